@@ -38,7 +38,7 @@ def listed():
         # head of a 128 x 6 row verify step: compute bound
         dict(name="gemm_head_decode", op="gemm", M=768, N=154880, K=6144, w_rows=128, out="bfloat16"),
         # --- logits to the acceptance's inputs
-        # one request without drafts, a small vocabulary, temperature only: latency
+        # one request without drafts, a small vocabulary, penalties and temperature: latency
         dict(name="logits_one_row", op="logits", B=1, K=0, V=32000, logits="bfloat16", penalties=True, bias=0, mask="none",
              probs=True, processed=False),
         # odd vocabulary, everything on, the processed logits kept too
