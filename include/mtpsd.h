@@ -64,6 +64,7 @@ extern "C" {
 #define MTPSD_STATUS_WRITE_RANGE 2   /* a write-back row outside the pool (skipped) */
 #define MTPSD_STATUS_WAIT_TIMEOUT 4  /* a bounded device wait expired (kernel gave up) */
 #define MTPSD_STATUS_ROW_RANGE 8     /* a row position outside its request's pool rows (skipped) */
+#define MTPSD_STATUS_EMPTY_ROW 16    /* a logits row in which nothing is allowed (argmax -1, probabilities 0) */
 
 /* ------------------------------------------------------------------------
  * Ragged token merge.  [P4] "Token 合并:RaggedTokenMerger 与 ragged_token_merger"
@@ -440,6 +441,114 @@ int mtpsd_sparse_mla_decode_paged(const mtpsd_mla_args* args, const mtpsd_paged_
 int mtpsd_topk_share_gather(const int32_t* step0_topk, const uint32_t* row_offsets,
                             const int32_t* num_accepted, int32_t B, int32_t k, int32_t* shared_idx,
                             const int64_t* row_pos, int64_t* shared_pos, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Matrix product of FP8 E4M3 codes with a float32 scale for each block of 128
+ * values of K (the projections and the head of an FP8 model; the codes and
+ * scales that mtpsd_quantize_fp8_block128 makes of the hidden states, [P3]
+ * "Indexer 的结构与计算流程" for the block size):
+ *   out[m,n] = sum_kb a_scale[m,kb] * w_scale[n',kb] * sum_{k in block kb} a[m,k] * w[n,k]
+ *   a [M, K] uint8, a_scale [M, K/128] float32       w [N, K] uint8
+ *   w_scale [N, K/128] float32 (w_scale_rows 1: n' = n, the quantizer's blocks) or
+ *           [ceil(N/128), K/128] (w_scale_rows 128: n' = n / 128, blocks of 128 x 128)
+ *   out [M, N], out_dtype MTPSD_BF16 or MTPSD_F32, row stride ld_out (elements, >= N)
+ * Each block's sum and the sum over the blocks are held in float32; the result is rounded
+ * once to out_dtype.  The order of the sums depends on M, N and K only.
+ * K is a multiple of 128; a and w are 16-byte aligned, out to its element; M, N < 2^31.
+ * M = 0 or N = 0 launches nothing; K = 0 writes zeros.  A NaN code (0x7F, 0xFF) or a scale that is
+ * not finite reaches the outputs of its own row m and column n and no others.
+ */
+int mtpsd_gemm_fp8_block128(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                            int32_t w_scale_rows, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* out,
+                            int64_t ld_out, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token table of the repetition, frequency and presence penalties: one int16
+ * word per request and token of the vocabulary,
+ *   counts [n_rows, ld], ld >= mtpsd_token_counts_ld(V) and a multiple of 8, 16-byte aligned;
+ *   the sign bit: the token occurs in the request's prompt; the low 15 bits: how often the request
+ *   has put it out, held at 32767.
+ * Request b uses row count_rows[b] (int32 [B], distinct), or row b when count_rows is NULL (then
+ * n_rows >= B); -1 marks a request without a row.  A row outside [-1, n_rows) is skipped and
+ * flagged MTPSD_STATUS_ROW_RANGE, a row that an earlier request of the call has too is skipped and flagged
+ * MTPSD_STATUS_INDEX_RANGE (build), a token outside [0, V) is skipped and flagged MTPSD_STATUS_INDEX_RANGE.
+ */
+int64_t mtpsd_token_counts_ld(int64_t V);   /* V rounded up to 8 */
+
+/* Builds the rows of B requests from their tokens (the rows' old contents are dropped; columns V .. ld - 1
+ * become 0):
+ *   tokens [S] int64, request b's are tokens[offsets[b] .. offsets[b+1]-1] (offsets uint32 [B+1], the
+ *   prefix sums of mtpsd_merge_tokens); its first n_prompt[b] (int64 [B]; NULL: all of them) are the
+ *   prompt, the others output.
+ * Offsets past S are cut to S and flagged MTPSD_STATUS_ROW_RANGE; a segment that ends before it starts is empty. */
+int mtpsd_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* offsets, const int64_t* n_prompt,
+                             int32_t B, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
+                             const int32_t* count_rows, int32_t* dev_status, void* stream);
+
+/* Adds the tokens that a step has put out: draft[b, 0 .. num_accepted[b]-1] and next_tokens[b]
+ * (draft [B, K] int64, num_accepted [B] int32 clamped to [0, K], next_tokens [B] int64: the outputs of
+ * mtpsd_accept_greedy and mtpsd_accept_stochastic).  K may be 0 (draft and num_accepted NULL: single tokens). */
+int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted, const int64_t* next_tokens,
+                              int32_t B, int32_t K, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
+                              const int32_t* count_rows, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Logits of the verify rows to the acceptance's inputs: penalties for repeated tokens, biases, the
+ * grammar mask ([P1] "阶段 3:拒绝采样与 Bitmask"), then the greedy token (target_argmax of
+ * mtpsd_accept_greedy) and the target distribution (target_probs of mtpsd_accept_stochastic).
+ * Row r is local row i of request b (row_offsets); token t of it, in float32 and in this order:
+ *   n = (counts word & 32767) + #{ j < min(i, K) : draft[b, j] = t }       (row i follows i drafts)
+ *   x = logits[r, t]
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]     when t is in the prompt or n > 0
+ *   x = x - frequency[b] * n,   then x - presence[b] when n > 0
+ *   x = x + bias                                           for each of the request's biases of t, in list order
+ *   x = -inf                                               where the row's mask bit is 0, whatever x was
+ *   out_logits[r, t] = x
+ *   argmax[r] = the lowest t of the largest x
+ *   probs[r, t] = exp((x - max) / temperature[b]) / sum    (one-hot at argmax when temperature[b] is not > 0)
+ * Every input after row_offsets may be NULL and is then left out (repetition 1, temperature 1, ...); so may
+ * each output, but not all three.  A row in which every x is -inf gets argmax -1 and probabilities 0 and is
+ * flagged MTPSD_STATUS_EMPTY_ROW.  Entries of +inf share the mass equally.  A NaN that is not masked makes the row's
+ * probabilities NaN (one-hot at temperature 0) and argmax its first position.  Rows outside
+ * row_offsets[0] .. row_offsets[B]-1 (a padded batch) are left as they were.
+ * Bad device values are skipped and flagged: draft and bias tokens outside [0, V) and bias offsets past
+ * n_bias MTPSD_STATUS_INDEX_RANGE; count_rows (as the token table; -1: nothing counted) and mask_rows (-1: no mask)
+ * outside their arrays MTPSD_STATUS_ROW_RANGE.  V <= 393216.
+ */
+typedef struct {
+  int32_t B;                   /* requests */
+  int32_t R;                   /* rows that the arrays hold (>= row_offsets[B]; at most 2^24) */
+  int64_t V;                   /* vocabulary */
+  int32_t dtype;               /* MTPSD_F32 or MTPSD_BF16: logits */
+  int32_t K;                   /* drafts per request (columns of draft) */
+  const void* logits;          /* [R, V], row stride ld */
+  int64_t ld;                  /* >= V (elements) */
+  const uint32_t* row_offsets; /* [B+1] */
+  const int16_t* counts;       /* [counts_rows, counts_ld] token table, or NULL */
+  int64_t counts_ld;
+  int32_t counts_rows;
+  int32_t n_bias;              /* entries of bias_tokens and bias_values */
+  const int32_t* count_rows;   /* [B] or NULL */
+  const int64_t* draft;        /* [B, K] or NULL (K 0) */
+  const float* repetition;     /* [B] or NULL */
+  const float* frequency;      /* [B] or NULL */
+  const float* presence;       /* [B] or NULL */
+  const uint32_t* bias_offsets; /* [B+1] or NULL: request b's biases are entries bias_offsets[b] .. bias_offsets[b+1]-1 */
+  const int32_t* bias_tokens;  /* [n_bias] */
+  const float* bias_values;    /* [n_bias] */
+  const int32_t* bitmask;      /* [n_masks, ceil(V/32)] or NULL: bit t % 32 of word t / 32 is 1 where t is allowed */
+  const int32_t* mask_rows;    /* [R] or NULL: the mask of each row (NULL: mask r, n_masks >= R) */
+  int32_t n_masks;
+  const float* temperature;    /* [B] or NULL */
+  int64_t* argmax;             /* [R] or NULL */
+  float* probs;                /* [R, V], row stride probs_ld, or NULL */
+  int64_t probs_ld;
+  float* out_logits;           /* [R, V], row stride out_ld, or NULL; may be logits itself (MTPSD_F32, out_ld = ld) */
+  int64_t out_ld;
+  int32_t* dev_status;         /* nullable */
+} mtpsd_logits_args;
+
+int mtpsd_process_logits(const mtpsd_logits_args* args, void* stream);
 
 /* ------------------------------------------------------------------------
  * Check of the device-side bounded wait (the source pages have no

@@ -28,6 +28,7 @@ STATUS_INDEX_RANGE = 1
 STATUS_WRITE_RANGE = 2
 STATUS_WAIT_TIMEOUT = 4
 STATUS_ROW_RANGE = 8
+STATUS_EMPTY_ROW = 16
 
 vp = C.c_void_p
 i32 = C.c_int32
@@ -56,6 +57,17 @@ class MlaArgs(C.Structure):
 
 class PagedKV(C.Structure):
     _fields_ = [("block_table", vp), ("bt_stride", i32), ("page_size", i32)]
+
+
+class LogitsArgs(C.Structure):
+    _fields_ = [
+        ("B", i32), ("R", i32), ("V", i64), ("dtype", i32), ("K", i32), ("logits", vp), ("ld", i64),
+        ("row_offsets", vp), ("counts", vp), ("counts_ld", i64), ("counts_rows", i32), ("n_bias", i32),
+        ("count_rows", vp), ("draft", vp), ("repetition", vp), ("frequency", vp), ("presence", vp),
+        ("bias_offsets", vp), ("bias_tokens", vp), ("bias_values", vp), ("bitmask", vp), ("mask_rows", vp),
+        ("n_masks", i32), ("temperature", vp), ("argmax", vp), ("probs", vp), ("probs_ld", i64),
+        ("out_logits", vp), ("out_ld", i64), ("dev_status", vp),
+    ]
 
 
 # name -> (restype, argtypes); every symbol include/mtpsd.h declares
@@ -90,6 +102,11 @@ SIGNATURES = {
     "mtpsd_indexer_scores_paged": (C.c_int, [C.POINTER(IndexerArgs), C.POINTER(PagedKV), vp]),
     "mtpsd_sparse_mla_decode_paged": (C.c_int, [C.POINTER(MlaArgs), C.POINTER(PagedKV), vp]),
     "mtpsd_topk_share_gather": (C.c_int, [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]),
+    "mtpsd_gemm_fp8_block128": (C.c_int, [vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp, vp]),
+    "mtpsd_token_counts_ld": (i64, [i64]),
+    "mtpsd_token_counts_build": (C.c_int, [vp, i64, vp, vp, i32, i64, vp, i64, i32, vp, vp, vp]),
+    "mtpsd_token_counts_accept": (C.c_int, [vp, vp, vp, i32, i32, i64, vp, i64, i32, vp, vp, vp]),
+    "mtpsd_process_logits": (C.c_int, [C.POINTER(LogitsArgs), vp]),
     "mtpsd_check_bounded_wait": (C.c_int, [i64, vp, vp, vp]),
     "mtpsd_last_error": (C.c_char_p, []),
     "mtpsd_version": (i32, []),

@@ -485,3 +485,226 @@ def kv_writeback_slots(src_latent, src_idxk, src_idxs, num_accepted, dst_latent,
         _ptr(num_accepted), _ptr(dst_latent), _ptr(dst_idxk), _ptr(dst_idxs), _ptr(dst_slots), dst_latent.shape[0],
         _ptr(dst_pos), _ptr(next_pos), _ptr(dev_status), _stream(stream)))
     return next_pos
+
+
+# --------------------------------------------------------------------------- head and logits
+
+def _need_rows(t, name: str, dtypes, shape):
+    """A 2-D CUDA tensor of the given shape whose rows are contiguous (any row stride >= the row)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _here(*tensors):
+    """Every tensor on the current device: the launch goes to the current device's stream."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _need_status(t):
+    if t is not None:
+        _need(t, "dev_status", torch.int32)
+        if t.numel() < 1:
+            raise ValueError("dev_status must hold one int32")
+
+
+def gemm_fp8_block128(a, a_scale, w, w_scale, out=None, out_dtype=None, dev_status=None, stream=None):
+    """out [M, N] = the product of E4M3 codes a [M, K] and w [N, K] (uint8) with a float32 scale per block of 128:
+    a_scale [M, K/128]; w_scale [N, K/128] (quantize_fp8_block128 of the weight) or [ceil(N/128), K/128] (128 x 128
+    blocks).  out is bf16 (or out_dtype float32); an out given may have any row stride."""
+    _need(a, "a", torch.uint8, 2)
+    _need(w, "w", torch.uint8, 2)
+    M, K = a.shape
+    n_out = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError("a and w must have the same K")
+    if K % 128:
+        raise ValueError("K must be a multiple of 128")
+    _need(a_scale, "a_scale", torch.float32)
+    _need(w_scale, "w_scale", torch.float32, 2)
+    if a_scale.shape not in ((M, K // 128), (M * (K // 128),)):
+        raise ValueError("a_scale must be [M, K/128]")
+    if w_scale.shape == (n_out, K // 128):
+        rows = 1
+    elif w_scale.shape == (-(-n_out // 128), K // 128):
+        rows = 128
+    else:
+        raise ValueError("w_scale must be [N, K/128] or [ceil(N/128), K/128]")
+    if out is None:
+        out = torch.empty(M, n_out, dtype=out_dtype or torch.bfloat16, device=a.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    _need_rows(out, "out", (torch.bfloat16, torch.float32), (M, n_out))
+    _need_status(dev_status)
+    _here(a, a_scale, w, w_scale, out, dev_status)
+    check("mtpsd_gemm_fp8_block128", lib().mtpsd_gemm_fp8_block128(
+        _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), rows, M, n_out, K,
+        N.MTPSD_F32 if out.dtype == torch.float32 else N.MTPSD_BF16, _ptr(out), _row_stride(out), _ptr(dev_status),
+        _stream(stream)))
+    return out
+
+
+def token_counts_ld(V: int) -> int:
+    """Row stride (int16 words) of a token table of V tokens."""
+    return int(lib().mtpsd_token_counts_ld(V))
+
+
+def _need_counts(counts, V, B, count_rows):
+    _need(counts, "counts", torch.int16, 2)
+    if counts.shape[1] < V or counts.shape[1] % 8:
+        raise ValueError("counts rows must have at least V words, a multiple of 8 (token_counts_ld)")
+    if count_rows is not None:
+        _need(count_rows, "count_rows", torch.int32, 1)
+        if count_rows.numel() != B:
+            raise ValueError("count_rows must have one entry per request")
+    elif counts.shape[0] < B:
+        raise ValueError("counts has fewer rows than requests")
+
+
+def token_counts_build(tokens, offsets, V: int, n_prompt=None, counts=None, count_rows=None, dev_status=None,
+                       stream=None):
+    """The token table rows of B requests from their tokens [S] int64 (ragged, offsets [B+1] uint32): the first
+    n_prompt[b] (int64; all without it) set the prompt bit, the others count as output.  Request b fills row b, or
+    count_rows[b] of a larger table."""
+    _need(tokens, "tokens", torch.int64, 1)
+    _need(offsets, "offsets", torch.uint32, 1)
+    B = offsets.numel() - 1
+    if B < 0:
+        raise ValueError("offsets must have B+1 entries")
+    if n_prompt is not None:
+        _need(n_prompt, "n_prompt", torch.int64, 1)
+        if n_prompt.numel() != B:
+            raise ValueError("n_prompt must have one entry per request")
+    if counts is None:
+        if count_rows is not None:
+            raise ValueError("count_rows needs a table")
+        counts = torch.empty(B, token_counts_ld(V), dtype=torch.int16, device=tokens.device)
+    _need_counts(counts, V, B, count_rows)
+    _need_status(dev_status)
+    _here(tokens, offsets, n_prompt, counts, count_rows, dev_status)
+    check("mtpsd_token_counts_build", lib().mtpsd_token_counts_build(
+        _ptr(tokens), tokens.numel(), _ptr(offsets), _ptr(n_prompt), B, V, _ptr(counts), counts.shape[1],
+        counts.shape[0], _ptr(count_rows), _ptr(dev_status), _stream(stream)))
+    return counts
+
+
+def token_counts_accept(counts, V: int, draft, num_accepted, next_tokens, count_rows=None, dev_status=None, stream=None):
+    """Adds draft[b, :num_accepted[b]] and next_tokens[b] to the token table (in place); draft and num_accepted may be
+    None (one token per request)."""
+    _need(next_tokens, "next_tokens", torch.int64, 1)
+    B = next_tokens.numel()
+    K = 0
+    if (draft is None) != (num_accepted is None):
+        raise ValueError("give draft and num_accepted together or neither")
+    if draft is not None:
+        _need(draft, "draft", torch.int64, 2)
+        _need(num_accepted, "num_accepted", torch.int32, 1)
+        K = draft.shape[1]
+        if draft.shape[0] != B or num_accepted.numel() != B:
+            raise ValueError("draft [B, K], num_accepted [B] and next_tokens [B] must have the same B")
+    _need_counts(counts, V, B, count_rows)
+    _need_status(dev_status)
+    _here(counts, draft, num_accepted, next_tokens, count_rows, dev_status)
+    check("mtpsd_token_counts_accept", lib().mtpsd_token_counts_accept(
+        _ptr(draft), _ptr(num_accepted), _ptr(next_tokens), B, K, V, _ptr(counts), counts.shape[1], counts.shape[0],
+        _ptr(count_rows), _ptr(dev_status), _stream(stream)))
+    return counts
+
+
+def process_logits(logits, row_offsets, draft=None, counts=None, count_rows=None, repetition=None, frequency=None,
+                   presence=None, bias_offsets=None, bias_tokens=None, bias_values=None, bitmask=None, mask_rows=None,
+                   temperature=None, argmax=None, probs=None, out_logits=None, dev_status=None, stream=None):
+    """Penalties, biases and grammar masks on logits [R, V] (bf16 or float32, any row stride), then the outputs given:
+    argmax [R] int64, probs [R, V] float32, out_logits [R, V] float32 (may be logits itself).  With none given, argmax
+    is allocated.  Returns argmax.
+
+    draft [B, K] int64 (row i of a request counts its first i drafts as output); counts: the token table (rows by
+    request, or count_rows [B] int32); repetition, frequency, presence, temperature [B] float32; biases as ragged lists
+    (bias_offsets [B+1] uint32, bias_tokens int32, bias_values float32); bitmask [n, ceil(V/32)] int32, one row per
+    logits row, or mask_rows [R] int32 (-1: none)."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch tensor")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [R, V]")
+    R, V = logits.shape
+    _need_rows(logits, "logits", (torch.bfloat16, torch.float32), (R, V))
+    _need(row_offsets, "row_offsets", torch.uint32, 1)
+    B = row_offsets.numel() - 1
+    K = 0
+    if draft is not None:
+        _need(draft, "draft", torch.int64, 2)
+        if draft.shape[0] != B:
+            raise ValueError("draft must be [B, K]")
+        K = draft.shape[1]
+    if counts is not None:
+        _need_counts(counts, V, B, count_rows)
+    elif count_rows is not None:
+        raise ValueError("count_rows without counts")
+    for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence),
+                    ("temperature", temperature)):
+        if t is not None:
+            _need(t, name, torch.float32, 1)
+            if t.numel() != B:
+                raise ValueError(f"{name} must have one entry per request")
+    given = [t is not None for t in (bias_offsets, bias_tokens, bias_values)]
+    if any(given) and not all(given):
+        raise ValueError("give bias_offsets, bias_tokens and bias_values together or none")
+    if bias_offsets is not None:
+        _need(bias_offsets, "bias_offsets", torch.uint32, 1)
+        _need(bias_tokens, "bias_tokens", torch.int32, 1)
+        _need(bias_values, "bias_values", torch.float32, 1)
+        if bias_offsets.numel() != B + 1 or bias_tokens.numel() != bias_values.numel():
+            raise ValueError("bias_offsets must be [B+1], bias_tokens and bias_values of one length")
+    if bitmask is not None:
+        _need(bitmask, "bitmask", torch.int32, 2)
+        if bitmask.shape[1] != -(-V // 32):
+            raise ValueError("bitmask rows must have ceil(V/32) words")
+    if mask_rows is not None:
+        _need(mask_rows, "mask_rows", torch.int32, 1)
+        if mask_rows.numel() != R:
+            raise ValueError("mask_rows must have one entry per row")
+    if argmax is None and probs is None and out_logits is None:
+        argmax = torch.empty(R, dtype=torch.int64, device=logits.device)
+    if argmax is not None:
+        _need(argmax, "argmax", torch.int64)
+        if argmax.numel() != R:
+            raise ValueError("argmax must have one entry per row")
+    for name, t in (("probs", probs), ("out_logits", out_logits)):
+        if t is not None:
+            _need_rows(t, name, (torch.float32,), (R, V))
+    _need_status(dev_status)
+    _here(logits, row_offsets, draft, counts, count_rows, repetition, frequency, presence, bias_offsets, bias_tokens,
+          bias_values, bitmask, mask_rows, temperature, argmax, probs, out_logits, dev_status)
+
+    def p(t):
+        return None if t is None else t.data_ptr()
+
+    a = N.LogitsArgs(B=B, R=R, V=V, dtype=N.MTPSD_F32 if logits.dtype == torch.float32 else N.MTPSD_BF16, K=K,
+                     logits=p(logits), ld=_row_stride(logits), row_offsets=p(row_offsets), counts=p(counts),
+                     counts_ld=0 if counts is None else counts.shape[1],
+                     counts_rows=0 if counts is None else counts.shape[0],
+                     n_bias=0 if bias_tokens is None else bias_tokens.numel(), count_rows=p(count_rows), draft=p(draft),
+                     repetition=p(repetition), frequency=p(frequency), presence=p(presence),
+                     bias_offsets=p(bias_offsets), bias_tokens=p(bias_tokens), bias_values=p(bias_values),
+                     bitmask=p(bitmask), mask_rows=p(mask_rows), n_masks=0 if bitmask is None else bitmask.shape[0],
+                     temperature=p(temperature), argmax=p(argmax), probs=p(probs),
+                     probs_ld=0 if probs is None else _row_stride(probs), out_logits=p(out_logits),
+                     out_ld=0 if out_logits is None else _row_stride(out_logits), dev_status=p(dev_status))
+    check("mtpsd_process_logits", lib().mtpsd_process_logits(C.byref(a), _stream(stream)))
+    return argmax

@@ -50,7 +50,7 @@ extern "C" {
 
 const char* mtpsd_last_error(void) { return g_err; }
 
-int32_t mtpsd_version(void) { return 102; }
+int32_t mtpsd_version(void) { return 103; }
 
 int mtpsd_merge_tokens(const int64_t* prompt_tokens, int64_t S, const uint32_t* prompt_offsets,
                        const int64_t* draft_tokens, int32_t B, int32_t K, int64_t* merged_tokens,
@@ -411,6 +411,92 @@ int mtpsd_topk_share_gather(const int32_t* step0_topk, const uint32_t* row_offse
     return fail(MTPSD_EINVAL, "topk_share_gather: buffers must be 16-byte aligned when k % 4 == 0");
   return launch_share_gather(step0_topk, row_offsets, num_accepted, B, k, shared_idx, row_pos, shared_pos, dev_status,
                              (cudaStream_t)stream);
+}
+
+int mtpsd_gemm_fp8_block128(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                            int32_t w_scale_rows, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* out,
+                            int64_t ld_out, int32_t* dev_status, void* stream) {
+  g_err[0] = 0;
+  if (M < 0 || N < 0 || K < 0 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+    return fail(MTPSD_EINVAL, "gemm_fp8_block128: M, N and K must be in 0..2^31-1");
+  if (K % 128) return fail(MTPSD_EUNSUPPORTED, "gemm_fp8_block128: K must be a multiple of 128");
+  if (w_scale_rows != 1 && w_scale_rows != 128) return fail(MTPSD_EUNSUPPORTED, "gemm_fp8_block128: w_scale_rows must be 1 or 128");
+  if (out_dtype != MTPSD_BF16 && out_dtype != MTPSD_F32)
+    return fail(MTPSD_EUNSUPPORTED, "gemm_fp8_block128: out_dtype must be MTPSD_BF16 or MTPSD_F32");
+  if (ld_out < N) return fail(MTPSD_EINVAL, "gemm_fp8_block128: ld_out < N");
+  if (M == 0 || N == 0) return MTPSD_OK;
+  if (!out || (K > 0 && (!a || !a_scale || !w || !w_scale))) return fail(MTPSD_EINVAL, "gemm_fp8_block128: null pointer");
+  if (!aligned(a, 16) || !aligned(w, 16)) return fail(MTPSD_EINVAL, "gemm_fp8_block128: a and w must be 16-byte aligned");
+  if (!aligned(out, out_dtype == MTPSD_F32 ? 4 : 2) || !aligned(a_scale, 4) || !aligned(w_scale, 4))
+    return fail(MTPSD_EINVAL, "gemm_fp8_block128: out and the scales must be aligned to their elements");
+  GemmFp8Plan p;
+  p.a = a; p.a_scale = a_scale; p.w = w; p.w_scale = w_scale; p.w_scale_rows = w_scale_rows;
+  p.M = M; p.N = N; p.K = K; p.out_f32 = out_dtype == MTPSD_F32; p.out = out; p.ld_out = ld_out; p.status = dev_status;
+  return launch_gemm_fp8(p, (cudaStream_t)stream);
+}
+
+int64_t mtpsd_token_counts_ld(int64_t V) { return V > 0 ? (V + 7) / 8 * 8 : 0; }
+
+// The checks that the calls on the token table share.
+static int check_counts(const void* counts, int64_t V, int64_t ld, int32_t n_rows, int32_t B, bool has_rows, const char* who) {
+  if (V < 1 || V > 0x7fffffffLL) return fail(MTPSD_EINVAL, "%s: need 1 <= V < 2^31", who);
+  if (!counts || !aligned(counts, 16)) return fail(MTPSD_EINVAL, "%s: counts must be given and 16-byte aligned", who);
+  if (ld < V || ld % 8) return fail(MTPSD_EINVAL, "%s: the table's row stride must be a multiple of 8 and at least V", who);
+  if (n_rows < 0 || (!has_rows && n_rows < B)) return fail(MTPSD_EINVAL, "%s: the table has fewer rows than requests", who);
+  return MTPSD_OK;
+}
+
+int mtpsd_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* offsets, const int64_t* n_prompt,
+                             int32_t B, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
+                             const int32_t* count_rows, int32_t* dev_status, void* stream) {
+  g_err[0] = 0;
+  if (B < 0 || S < 0 || S > 0xffffffffLL) return fail(MTPSD_EINVAL, "token_counts_build: need B >= 0, 0 <= S < 2^32");
+  if (B == 0) return MTPSD_OK;
+  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows != nullptr, "token_counts_build")) return rc;
+  if (!offsets || (S > 0 && !tokens)) return fail(MTPSD_EINVAL, "token_counts_build: null pointer");
+  return launch_token_counts_build(tokens, S, offsets, n_prompt, B, V, counts, ld, n_rows, count_rows, dev_status,
+                                   (cudaStream_t)stream);
+}
+
+int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted, const int64_t* next_tokens,
+                              int32_t B, int32_t K, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
+                              const int32_t* count_rows, int32_t* dev_status, void* stream) {
+  g_err[0] = 0;
+  if (B < 0 || K < 0 || (int64_t)B * ((int64_t)K + 1) > 0x7fffffffLL)
+    return fail(MTPSD_EINVAL, "token_counts_accept: need B >= 0, K >= 0, B * (K + 1) < 2^31");
+  if (B == 0) return MTPSD_OK;
+  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows != nullptr, "token_counts_accept")) return rc;
+  if (!next_tokens || (K > 0 && (!draft || !num_accepted))) return fail(MTPSD_EINVAL, "token_counts_accept: null pointer");
+  return launch_token_counts_accept(draft, num_accepted, next_tokens, B, K, V, counts, ld, n_rows, count_rows, dev_status,
+                                    (cudaStream_t)stream);
+}
+
+int mtpsd_process_logits(const mtpsd_logits_args* a, void* stream) {
+  g_err[0] = 0;
+  if (!a) return fail(MTPSD_EINVAL, "process_logits: null args");
+  if (a->B < 1 || a->R < 0 || a->K < 0) return fail(MTPSD_EINVAL, "process_logits: need B >= 1, R >= 0, K >= 0");
+  if (a->V < 1) return fail(MTPSD_EINVAL, "process_logits: need V >= 1");
+  if (a->V > 393216) return fail(MTPSD_EUNSUPPORTED, "process_logits: V > 393216");
+  if (a->R > (1 << 24)) return fail(MTPSD_EUNSUPPORTED, "process_logits: R > 2^24");
+  if (a->dtype != MTPSD_F32 && a->dtype != MTPSD_BF16)
+    return fail(MTPSD_EUNSUPPORTED, "process_logits: dtype must be MTPSD_F32 or MTPSD_BF16");
+  if (a->ld < a->V || (a->probs && a->probs_ld < a->V) || (a->out_logits && a->out_ld < a->V))
+    return fail(MTPSD_EINVAL, "process_logits: a row stride is below V");
+  if (a->R > 0 && !a->argmax && !a->probs && !a->out_logits) return fail(MTPSD_EINVAL, "process_logits: no output given");
+  if (a->counts)
+    if (int rc = check_counts(a->counts, a->V, a->counts_ld, a->counts_rows, a->B, a->count_rows != nullptr, "process_logits")) return rc;
+  if (a->bias_offsets && (a->n_bias < 0 || (a->n_bias > 0 && (!a->bias_tokens || !a->bias_values))))
+    return fail(MTPSD_EINVAL, "process_logits: biases need n_bias >= 0, bias_tokens and bias_values");
+  if (a->bitmask && (a->n_masks < 0 || (!a->mask_rows && a->n_masks < a->R)))
+    return fail(MTPSD_EINVAL, "process_logits: fewer masks than rows");
+  if (a->R == 0) return MTPSD_OK;
+  if (!a->logits || !a->row_offsets || (a->K > 0 && !a->draft)) return fail(MTPSD_EINVAL, "process_logits: null pointer");
+  const size_t es = a->dtype == MTPSD_F32 ? 4 : 2;
+  if (!aligned(a->logits, es) || !aligned(a->probs, 4) || !aligned(a->out_logits, 4))
+    return fail(MTPSD_EINVAL, "process_logits: logits, probs and out_logits must be aligned to their elements");
+  if ((const void*)a->out_logits == a->logits && (a->dtype != MTPSD_F32 || a->out_ld != a->ld))
+    return fail(MTPSD_EINVAL, "process_logits: in place needs float32 logits and out_ld == ld");
+  return launch_process_logits(*a, (cudaStream_t)stream);
 }
 
 int mtpsd_check_bounded_wait(int64_t limit_ns, int32_t* dev_status, int64_t* result, void* stream) {

@@ -555,3 +555,69 @@ class StochasticAccept:
 
     def launches_per_step(self) -> int:
         return 1
+
+
+class VerifyHead:
+    """The verify step from the rows' hidden states to the acceptance: FP8 product with the head's weight, penalties,
+    biases and grammar masks, greedy or rejection-sampling acceptance ([P1] "阶段 3:拒绝采样与 Bitmask"), and the token
+    table advanced by the accepted tokens.  B requests of K + 1 rows each.
+
+    weight, weight_scale: the head's codes [V, D] and block scales (gemm_fp8_block128); params: keyword arguments of
+    process_logits (repetition, temperature, bitmask, ...); draft_probs [B, K, V] with u_accept and u_sample switch to
+    rejection sampling.  The caller fills `hidden` [B (K+1), D] float32 and `draft` [B, K] before a step."""
+
+    def __init__(self, weight, weight_scale, B: int, K: int, counts=None, params=None, draft_probs=None, u_accept=None,
+                 u_sample=None, logits_dtype=torch.bfloat16):
+        device = weight.device
+        V, D = weight.shape
+        R = B * (K + 1)
+        self.weight, self.weight_scale = weight, weight_scale
+        self.B, self.K, self.R, self.V, self.D = B, K, R, V, D
+        self.counts, self.params = counts, dict(params or {})
+        self.draft_probs, self.u_accept, self.u_sample = draft_probs, u_accept, u_sample
+        self.hidden = torch.zeros(R, D, dtype=torch.float32, device=device)
+        self.draft = torch.zeros(B, K, dtype=torch.int64, device=device)
+        self.row_offsets = _dev_u32(np.arange(0, R + 1, K + 1), device)
+        self.h_codes = torch.empty(R, D, dtype=torch.uint8, device=device)
+        self.h_scale = torch.empty(R, D // 128, dtype=torch.float32, device=device)
+        self.logits = torch.empty(R, V, dtype=logits_dtype, device=device)
+        self.target_argmax = torch.empty(B, K + 1, dtype=torch.int64, device=device)
+        self.target_probs = torch.empty(B, K + 1, V, dtype=torch.float32, device=device) if draft_probs is not None \
+            else None
+        self.num_accepted = torch.empty(B, dtype=torch.int32, device=device)
+        self.next_tokens = torch.empty(B, dtype=torch.int64, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def project(self, stream=None):
+        api.quantize_fp8_block128(self.hidden, self.h_codes, self.h_scale, stream=stream)
+        api.gemm_fp8_block128(self.h_codes, self.h_scale, self.weight, self.weight_scale, out=self.logits,
+                              dev_status=self.status, stream=stream)
+
+    def process(self, stream=None):
+        probs = None if self.target_probs is None else self.target_probs.view(self.R, self.V)
+        api.process_logits(self.logits, self.row_offsets, draft=self.draft, counts=self.counts, argmax=self.target_argmax,
+                           probs=probs, dev_status=self.status, stream=stream, **self.params)
+
+    def accept(self, stream=None):
+        if self.draft_probs is None:
+            api.accept_greedy(self.draft, self.target_argmax, -1, self.num_accepted, self.next_tokens, stream=stream)
+        else:
+            api.accept_stochastic(self.draft, self.draft_probs, self.target_probs, self.u_accept, self.u_sample,
+                                  self.num_accepted, self.next_tokens, dev_status=self.status, stream=stream)
+
+    def commit(self, stream=None):
+        api.token_counts_accept(self.counts, self.V, self.draft, self.num_accepted, self.next_tokens,
+                                count_rows=self.params.get("count_rows"), dev_status=self.status, stream=stream)
+
+    def phases(self):
+        ph = [("project", self.project), ("process", self.process), ("accept", self.accept)]
+        if self.counts is not None:
+            ph.append(("commit", self.commit))
+        return ph
+
+    def step(self, stream=None):
+        for _, fn in self.phases():
+            fn(stream)
+
+    def launches_per_step(self) -> int:
+        return 4 + (self.counts is not None)

@@ -39,4 +39,8 @@ Pinning (what each function is checked against, other than itself) lives in
   kv_writeback_slots — pinned (hand-worked block tables, a paged pool built
   page by page reads back the contiguous cache, a swap that an in-place copy
   gets wrong, the contiguous write-back as a special case)
+* gemm.gemm_fp8_block128 — pinned (dequantized library product, hand-worked
+  blocks, one-hot codes)
+* logits.process_row / token_counts_build / token_counts_accept — pinned
+  (hand-worked rows and tables, softmax of the library, masked NaN)
 """
