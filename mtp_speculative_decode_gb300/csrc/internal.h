@@ -57,6 +57,7 @@ struct GemmFp8Plan {
   int32_t* status;
 };
 int launch_gemm_fp8(const GemmFp8Plan& p, cudaStream_t st);
+int launch_gemm_fp8_pair(const GemmFp8Plan& p, cudaStream_t st);   // many rows: pairs of CTAs (K > 0)
 
 // logits of the verify rows and the token table of their penalties
 int launch_process_logits(const mtpsd_logits_args& a, cudaStream_t st);

@@ -11,62 +11,61 @@
 // One MMA has M = 128 weight rows (operand A) and N = up to 256 rows of a
 // (operand B), so the rarely-many rows of a cost only as much as there are of
 // them and the weight streams through once: a tile is 128 outputs x `cols` rows
-// (cols: the rows cut into equal tiles of at most 256, rounded up to 16).  TMEM
-// lane = output, column = row of a: an epilogue thread's outputs share their
-// weight row, the row scales of a are broadcast reads of shared memory, and a
-// warp stores 32 consecutive outputs.
+// (cols: the rows cut into equal tiles of at most 256, rounded up to 16).
 //
-// Roles (352 threads, one CTA per SM):
-//   warps 0-7   epilogue: warp w reads the TMEM lanes 32 (w % 4) .. +31 and the columns of half w / 4.
-//   warp 8      TMA producer: a ring of stages of one block (128 x 128 bytes of w, cols x 128 of a).
-//   warp 9      TMEM allocation and MMA issue.
-//   warp 10     scales: a ring of slots of four blocks' scales; with 128 x 128 weight blocks it
+// The epilogue reads TMEM (lane = output, column = row of a) in the 16x256b
+// shape: a thread gets four lanes of every fourth column pair, so one 8-byte
+// shared-memory read of two column scales serves eight values.  (With one lane
+// per thread every scale is a broadcast read for one value: the reads took more
+// shared-memory cycles than the MMAs' operands, 290 against 186 us without them
+// at 192 x 154880 x 6144.)
+//
+// Roles (608 threads, one CTA per SM):
+//   warps 0-15  epilogue: warp w takes the TMEM lanes 32 (w % 4) .. +31 and the columns of quarter w / 4
+//               (four warps per scheduler hide the latency of the TMEM reads).
+//   warp 16     TMA producer: a ring of stages of one block (128 x 128 bytes of w, cols x 128 of a).
+//   warp 17     TMEM allocation and MMA issue.
+//   warp 18     scales: a ring of slots of four blocks' scales; with 128 x 128 weight blocks it
 //               multiplies the one weight scale of the tile's block in, else the slot holds the 128
 //               rows' scales too and the epilogue multiplies by its own.
 // With few tiles the blocks of K of a tile are split over a cluster of up to 8 CTAs (consecutive
 // runs of blocks), which add their accumulators through distributed shared memory in rank order.
 // The order of every sum is fixed by the sizes and the device.  Every mbarrier wait is bounded
 // (2 s): on expiry the kernel flags MTPSD_STATUS_WAIT_TIMEOUT, drains its copies, frees TMEM and returns.
-#include <cuda.h>
-#include <cuda_bf16.h>
-
 #include <algorithm>
 #include <string.h>
 
-#include "common.cuh"
-#include "internal.h"
-#include "mbar.cuh"
+#include "gemm_fp8.cuh"
 
 namespace mtpsd {
 namespace gtc {
 
 constexpr int TILE_N = 128;               // outputs (weight rows) per tile
-constexpr int KB = 128;                   // bytes of a block
-constexpr int EPI_WARPS = 8;
-constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, SCALE_WARP = 10;
-constexpr int THREADS = 32 * 11;
-constexpr int SG = 4;                     // blocks per scale slot
-constexpr int NSLOT = 4;                  // scale slots in flight
-constexpr int TMEM_COLS = 512;
+constexpr int EPI_WARPS = 16;
+constexpr int PRODUCER_WARP = 16, MMA_WARP = 17, SCALE_WARP = 18;
+constexpr int THREADS = 32 * 19;
 constexpr int MAX_SPLIT = 8;
 constexpr int W_BYTES = TILE_N * KB;
+constexpr int PAD_N = TILE_N + 4;         // row stride (floats) of a partial tile: a fragment's four columns miss each other's banks
+constexpr int TR_LD = 36;                 // the same for the transposed store of 8 columns x 32 outputs
+constexpr int TR_FLOATS = 8 * TR_LD;
 
-// NC: accumulator registers per epilogue thread / 32; a tile has at most 64 NC columns
+// NC: a tile has at most 64 NC columns, an epilogue thread 16 NC accumulators
 template <int NC>
 struct Shape {
   static constexpr int COLS = 64 * NC;
   static constexpr int STAGE = W_BYTES + COLS * KB;
-  static constexpr int NSTAGE = 200 * 1024 / STAGE;                     // 8, 6, 5, 4
-  static constexpr int BUF_COLS = NC == 3 ? 256 : COLS;                 // TMEM columns of one buffer
-  static constexpr int NBUF = TMEM_COLS / BUF_COLS;                     // 8, 4, 2, 2
+  static constexpr int NSTAGE = 192 * 1024 / STAGE;                     // 8, 6
+  static constexpr int NBUF = TMEM_COLS / COLS;                         // TMEM buffers: 8, 4
   static constexpr int SLOT_FLOATS = SG * (COLS + TILE_N);
   static constexpr int OFF_SCALE = NSTAGE * STAGE;
-  static constexpr int OFF_BAR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;
+  static constexpr int OFF_TR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;    // per epilogue warp: TR_FLOATS
+  static constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
   static constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;                    // + alignment slack
   static_assert(BYTES <= 232448, "shared memory per CTA");
-  static_assert(COLS * TILE_N * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
+  static_assert(COLS * PAD_N * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
   static_assert(OFF_BAR % 16 == 0, "barriers are aligned");
 };
 
@@ -84,110 +83,6 @@ struct Params {
   int32_t* status;
 };
 
-__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count));
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
-}
-// Warp-uniform bounded wait (all 32 lanes): false when it gave up.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar::wait<false>(bar, parity, abort_flag, status, mbar::DEFAULT_LIMIT_NS));
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(saddr(bar))
-      : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile("{\n .reg .b32 rx;\n .reg .pred px;\n elect.sync rx|px, 0xffffffff;\n selp.b32 %0, 1, 0, px;\n}\n"
-               : "=r"(pred));
-  return pred != 0;
-}
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row atoms of 1024 bytes, version 1.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_byte_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_byte_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-// Instruction descriptor: kind::f8f6f4, E4M3 x E4M3 -> F32, both K-major, M = 128, N = n (a multiple of 16).
-__device__ __forceinline__ uint32_t idesc_n(int n) { return (1u << 4) | ((uint32_t)n >> 3 << 17) | ((128u >> 4) << 24); }
-__device__ __forceinline__ void mma_fp8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t cta_addr, uint32_t rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(cta_addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-// Pairs of floats in one 64-bit register: the FMA pipe does both in one instruction.
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ void store_out(const Params& p, int64_t off, float v) {
   if (p.out_f32) ((float*)p.out)[off] = v;
   else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
@@ -250,8 +145,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
   const int first = (int)blockIdx.x / p.split, step = (int)gridDim.x / p.split;   // this cluster's tiles
   const int kb0 = (int)((int64_t)rank * p.kbs / p.split), kb1 = (int)((int64_t)(rank + 1) * p.kbs / p.split);
-  uint64_t acc[16 * NC];
-  constexpr int CH = NC == 4 ? 16 : 32;   // columns per TMEM read: with 128 accumulators there is no room for 32 more
+  // acc[4 j + 2 h + i]: columns 8 j + 2 (lane % 4), +1 of the warp's, output 16 h + 8 i + lane / 4 of its 32
+  float2 acc[8 * NC];
 
   if (warp == PRODUCER_WARP) {
     int n = 0;
@@ -292,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         tc_fence_after();
         if (elect_one()) {
           const uint32_t w_base = saddr(sm + stage * S::STAGE), a_base = w_base + W_BYTES;
-          const uint32_t d = tmem_base + (uint32_t)(buf * S::BUF_COLS);
+          const uint32_t d = tmem_base + (uint32_t)(buf * S::COLS);
 #pragma unroll
           for (int kk = 0; kk < KB / 32; ++kk)
             mma_fp8(d, sw128_desc(w_base + kk * 32), sw128_desc(a_base + kk * 32), id, kk > 0 ? 1u : 0u);
@@ -357,12 +252,14 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       }
     }
   } else {
-    const int quarter = warp & 3, c0 = (warp >> 2) * 32 * NC;      // this warp's TMEM lanes and first column
+    const int quarter = warp & 3, c0 = (warp >> 2) * 16 * NC;      // this warp's TMEM lanes and first column
+    const int fr = lane >> 2, fc = 2 * (lane & 3);                 // fragment row and column of this lane
+    const int mine = min(16 * NC, p.cols - c0);                    // columns of the tile (a multiple of 16; <= 0: none)
     int n = 0, ns = 0;
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step) {
 #pragma unroll
-      for (int i = 0; i < 16 * NC; ++i) acc[i] = 0ull;
+      for (int i = 0; i < 8 * NC; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
         const int slot = ns % NSLOT, j = (kb - kb0) % SG;
         if (j == 0) ok = wait_all(&s_full[slot], (ns / NSLOT) & 1, abort_flag, p.status);
@@ -370,36 +267,43 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         if (ok) ok = wait_all(&t_full[buf], (n / S::NBUF) & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const float* sc = scales + slot * S::SLOT_FLOATS + j * S::COLS + c0;
-        uint64_t rw = 0;
+        const float* sc = scales + slot * S::SLOT_FLOATS + j * S::COLS + c0 + fc;
+        float rw[4] = {1.f, 1.f, 1.f, 1.f};                        // the weight scales of the thread's four outputs
         if (ROWS1) {
-          const uint32_t r = __float_as_uint(scales[slot * S::SLOT_FLOATS + SG * S::COLS + j * TILE_N + quarter * 32 + lane]);
-          rw = pack2(r, r);
-        }
-        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * S::BUF_COLS + c0);
-        const int mine = min(32 * NC, p.cols - c0) + CH - 1;          // chunks with columns of the tile
+          const float* sr = scales + slot * S::SLOT_FLOATS + SG * S::COLS + j * TILE_N + quarter * 32 + fr;
 #pragma unroll
-        for (int c = 0; c < 32 * NC / CH; ++c) {
-          if ((c + 1) * CH > mine) break;
-          uint32_t t[CH];
-          if constexpr (CH == 32) tmem_ld32(taddr + CH * c, t);
-          else tmem_ld16(taddr + CH * c, t);
+          for (int i = 0; i < 4; ++i) rw[i] = sr[8 * i];
+        }
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * S::COLS + c0);
+#pragma unroll
+        for (int c = 0; c < 16 * NC; c += 32) {                    // 32 columns at a time, 16 at an odd end
+          const int w = 16 * NC - c < 32 ? 16 : 32;
+          if (c >= mine) break;
+          uint32_t t[2][16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (w == 32) tmem_ld_x4(taddr + ((uint32_t)(16 * h) << 16) + c, t[h]);
+            else tmem_ld_x2(taddr + ((uint32_t)(16 * h) << 16) + c, t[h]);
+          }
           tmem_ld_wait();
-          if ((c + 2) * CH > mine || c == 32 * NC / CH - 1) {      // the warp's last read of the buffer
+          if (c + 32 >= mine) {                                    // the warp's last read of the buffer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_empty[buf]);
           }
 #pragma unroll
-          for (int i = 0; i < CH / 4; ++i) {
-            const ulonglong2 s = *(const ulonglong2*)(sc + CH * c + 4 * i);
-            const uint64_t s0 = ROWS1 ? mul2(s.x, rw) : s.x, s1 = ROWS1 ? mul2(s.y, rw) : s.y;
-            uint64_t* q = acc + CH / 2 * c + 2 * i;
-            q[0] = fma2(pack2(t[4 * i], t[4 * i + 1]), s0, q[0]);
-            q[1] = fma2(pack2(t[4 * i + 2], t[4 * i + 3]), s1, q[1]);
+          for (int g = 0; g < w / 8; ++g) {
+            const float2 s = *(const float2*)(sc + c + 8 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2& q = acc[4 * (c / 8 + g) + i];
+              const uint32_t* v = t[i >> 1] + 4 * g + 2 * (i & 1);
+              q.x = fmaf(__uint_as_float(v[0]), ROWS1 ? s.x * rw[i] : s.x, q.x);
+              q.y = fmaf(__uint_as_float(v[1]), ROWS1 ? s.y * rw[i] : s.y, q.y);
+            }
           }
         }
-        if (mine < CH) {            // no columns: release the buffer at once
+        if (mine <= 0) {            // no columns: release the buffer at once
           __syncwarp();
           if (lane == 0) mbar_arrive(&t_empty[buf]);
         }
@@ -410,17 +314,29 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         }
       }
       if (!ok || p.split > 1) break;
+      // eight columns at a time through the warp's own shared memory, so that a store covers 32 consecutive outputs
       const int64_t n_out = (int64_t)(tile / p.n_mt) * TILE_N + quarter * 32 + lane;
-      const int m0 = tile % p.n_mt * p.cols + c0, m_end = min(p.M, tile % p.n_mt * p.cols + p.cols);
-      if (n_out < p.N) {
-        int64_t off = (int64_t)m0 * p.ld_out + n_out;
+      const int m0 = tile % p.n_mt * p.cols + c0;
+      const int m_cols = min(mine, p.M - m0);
+      float* tr = (float*)(sm + S::OFF_TR) + warp * TR_FLOATS;
+      int64_t off = (int64_t)m0 * p.ld_out + n_out;
 #pragma unroll
-        for (int i = 0; i < 16 * NC; ++i) {
-          const float2 v = unpack2(acc[i]);
-          if (m0 + 2 * i < m_end) store_out(p, off, v.x);
-          if (m0 + 2 * i + 1 < m_end) store_out(p, off + p.ld_out, v.y);
-          off += 2 * p.ld_out;
+      for (int g = 0; g < 2 * NC; ++g) {
+        if (8 * g >= m_cols) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = acc[4 * g + i];
+          tr[fc * TR_LD + 8 * i + fr] = v.x;
+          tr[(fc + 1) * TR_LD + 8 * i + fr] = v.y;
         }
+        __syncwarp();
+        if (n_out < p.N) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (8 * g + e < m_cols) store_out(p, off + e * p.ld_out, tr[e * TR_LD + lane]);
+        }
+        off += 8 * p.ld_out;
+        __syncwarp();
       }
     }
   }
@@ -429,16 +345,18 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   if (p.split > 1) {
     // The cluster's one tile: every rank's accumulators into its own stage ring (its copies and MMAs are
     // done: the epilogue has seen the last block), then each rank sums a part of the columns over the ranks.
-    float* part = (float*)sm;                               // [cols][128 outputs]
+    float* part = (float*)sm;                               // [cols][PAD_N]: 128 outputs
     __syncthreads();
     if (warp < EPI_WARPS) {
-      const int quarter = warp & 3, c0 = (warp >> 2) * 32 * NC;
+      const int c0 = (warp >> 2) * 16 * NC + 2 * (lane & 3), o = (warp & 3) * 32 + (lane >> 2);
 #pragma unroll
-      for (int i = 0; i < 16 * NC; ++i) {
-        const float2 v = unpack2(acc[i]);
-        part[(c0 + 2 * i) * TILE_N + quarter * 32 + lane] = v.x;
-        part[(c0 + 2 * i + 1) * TILE_N + quarter * 32 + lane] = v.y;
-      }
+      for (int g = 0; g < 2 * NC; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = acc[4 * g + i];
+          part[(c0 + 8 * g) * PAD_N + o + 8 * i] = v.x;
+          part[(c0 + 8 * g + 1) * PAD_N + o + 8 * i] = v.y;
+        }
     }
     cluster_sync();
     if (warp < EPI_WARPS) {
@@ -447,8 +365,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       const int r0 = (int)((int64_t)rank * m_cols / p.split), r1 = (int)((int64_t)(rank + 1) * m_cols / p.split);
       const int o = threadIdx.x & (TILE_N - 1);
       const int64_t n_out = (int64_t)(tile / p.n_mt) * TILE_N + o;
-      for (int c = r0 + (threadIdx.x >> 7); c < r1; c += 2) {
-        const uint32_t at = saddr(part + c * TILE_N + o);
+      for (int c = r0 + (threadIdx.x >> 7); c < r1; c += EPI_WARPS / 4) {
+        const uint32_t at = saddr(part + c * PAD_N + o);
         float v[MAX_SPLIT];
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r) v[r] = r < p.split ? ld_cluster(at, r) : 0.f;
@@ -473,17 +391,10 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Params);
 
 template <bool ROWS1>
 Kernel pick(int nc) {
-  switch (nc) {
-    case 1: return gemm_fp8_kernel<1, ROWS1>;
-    case 2: return gemm_fp8_kernel<2, ROWS1>;
-    case 3: return gemm_fp8_kernel<3, ROWS1>;
-    default: return gemm_fp8_kernel<4, ROWS1>;
-  }
+  return nc == 1 ? gemm_fp8_kernel<1, ROWS1> : gemm_fp8_kernel<2, ROWS1>;
 }
 
-int smem_bytes(int nc) {
-  return nc == 1 ? Shape<1>::BYTES : nc == 2 ? Shape<2>::BYTES : nc == 3 ? Shape<3>::BYTES : Shape<4>::BYTES;
-}
+int smem_bytes(int nc) { return nc == 1 ? Shape<1>::BYTES : Shape<2>::BYTES; }
 
 cudaLaunchConfig_t config(unsigned grid, int split, int nc, cudaStream_t st, cudaLaunchAttribute* attrs) {
   cudaLaunchConfig_t cfg = {};
@@ -514,8 +425,8 @@ int resident_clusters(int split) {
   }
   int n = 0;
   cudaLaunchAttribute attrs[2];
-  cudaLaunchConfig_t cfg = config((unsigned)split, split, 4, 0, attrs);
-  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel<4, false>, &cfg) != cudaSuccess) {
+  cudaLaunchConfig_t cfg = config((unsigned)split, split, 2, 0, attrs);
+  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel<2, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();            // not a fault of the call: such clusters are not used
     n = 0;
   }
@@ -543,16 +454,19 @@ int choose_split(int64_t tiles, int kbs) {
 
 }  // namespace gtc
 
+constexpr int64_t kPairRows = 128;
+
 int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   using namespace gtc;
   if (cc_major() != 10 || !tma_available()) {
     set_error("gemm_fp8_block128: needs a GPU of compute capability 10.x");
     return MTPSD_EUNSUPPORTED;
   }
+  if (g.M > kPairRows && g.K > 0) return launch_gemm_fp8_pair(g, st);
   Params p;
   p.sa = g.a_scale; p.sw = g.w_scale; p.out = g.out; p.ld_out = g.ld_out;
   p.M = (int)g.M; p.N = (int)g.N; p.kbs = (int)(g.K / KB);
-  p.n_mt = (int)ceil_div(g.M, 256);
+  p.n_mt = (int)ceil_div(g.M, 128);
   p.cols = (int)(ceil_div(ceil_div(g.M, p.n_mt), 16) * 16);
   const int64_t tiles = ceil_div(g.N, TILE_N) * p.n_mt;
   if (tiles > 0x3fffffffLL / MAX_SPLIT) {
@@ -574,9 +488,9 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   }
   const bool rows1 = g.w_scale_rows == 1;
   Kernel kern = rows1 ? pick<true>(nc) : pick<false>(nc);
-  static std::atomic<uint64_t> attr[8], attr4;
-  if (!set_smem_limit_once(kern, smem_bytes(nc), attr[(rows1 ? 4 : 0) + nc - 1]) ||
-      !set_smem_limit_once(gemm_fp8_kernel<4, false>, smem_bytes(4), attr4)) {
+  static std::atomic<uint64_t> attr[4], attr2;
+  if (!set_smem_limit_once(kern, smem_bytes(nc), attr[(rows1 ? 2 : 0) + nc - 1]) ||
+      !set_smem_limit_once(gemm_fp8_kernel<2, false>, smem_bytes(2), attr2)) {
     set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
   }
