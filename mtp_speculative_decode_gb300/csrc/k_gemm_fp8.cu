@@ -8,10 +8,13 @@
 // the epilogue warps read, scale and add to float32 accumulators in registers
 // while the next blocks' MMAs run into the other buffers.
 //
-// One MMA has M = 128 weight rows (operand A) and N = up to 256 rows of a
-// (operand B), so the rarely-many rows of a cost only as much as there are of
-// them and the weight streams through once: a tile is 128 outputs x `cols` rows
-// (cols: the rows cut into equal tiles of at most 256, rounded up to 16).
+// This kernel is for up to 128 rows of a (k_gemm_fp8_pair.cu takes more): one
+// MMA has M = 128 weight rows (operand A) and N = the rows of a, rounded up to
+// 16 (operand B), so the few rows of a cost only as much as there are of them
+// and the weight streams through once.  A tile is `bn` <= 128 outputs: the weight
+// read bounds these calls (16 x 154880 x 6144 runs at 97 % of the measured copy
+// rate), so bn is chosen such that the tiles load every SM alike; TMEM lanes
+// past bn hold products of stale operands and are not stored.
 //
 // The epilogue reads TMEM (lane = output, column = row of a) in the 16x256b
 // shape: a thread gets four lanes of every fourth column pair, so one 8-byte
@@ -25,22 +28,19 @@
 //               (four warps per scheduler hide the latency of the TMEM reads).
 //   warp 16     TMA producer: a ring of stages of one block (128 x 128 bytes of w, cols x 128 of a).
 //   warp 17     TMEM allocation and MMA issue.
-//   warp 18     scales: a ring of slots of four blocks' scales; with 128 x 128 weight blocks it
-//               multiplies the one weight scale of the tile's block in, else the slot holds the 128
-//               rows' scales too and the epilogue multiplies by its own.
+//   warp 18     scales: a ring of slots of four blocks' scales of the rows of a and of the weight rows.
 // With few tiles the blocks of K of a tile are split over a cluster of up to 8 CTAs (consecutive
 // runs of blocks), which add their accumulators through distributed shared memory in rank order.
 // The order of every sum is fixed by the sizes and the device.  Every mbarrier wait is bounded
 // (2 s): on expiry the kernel flags MTPSD_STATUS_WAIT_TIMEOUT, drains its copies, frees TMEM and returns.
 #include <algorithm>
-#include <string.h>
 
 #include "gemm_fp8.cuh"
 
 namespace mtpsd {
 namespace gtc {
 
-constexpr int TILE_N = 128;               // outputs (weight rows) per tile
+constexpr int TILE_N = 128;               // most outputs (weight rows) of a tile
 constexpr int EPI_WARPS = 16;
 constexpr int PRODUCER_WARP = 16, MMA_WARP = 17, SCALE_WARP = 18;
 constexpr int THREADS = 32 * 19;
@@ -75,8 +75,9 @@ struct Params {
   void* out;
   int64_t ld_out;
   int M, N, kbs;          // rows of a, outputs, blocks of K
-  int cols;               // columns of a tile (a multiple of 16)
-  int n_mt, tiles;        // tiles along M, tiles
+  int cols;               // columns of a tile: M rounded up to 16
+  int bn, tiles;          // outputs of a tile, tiles
+  int w_rows;             // weight rows that share a scale: 1 or 128
   int split;              // CTAs per cluster
   int out_f32;
   int vec_scales;         // a block row's scales can be read four at a time
@@ -88,8 +89,7 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t off, float v)
   else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
 }
 
-// ROWS1: the weight's scales are per row and block (else per 128 x 128 block).
-template <int NC, bool ROWS1>
+template <int NC>
 __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_w,
                                                               const __grid_constant__ CUtensorMap tmap_a,
                                                               const __grid_constant__ Params p) {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
                  "r"(TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (warp == PRODUCER_WARP && p.kbs > 0 && elect_one()) {
+  if (warp == PRODUCER_WARP && elect_one()) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmap_w) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmap_a) : "memory");
   }
@@ -146,14 +146,14 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   const int first = (int)blockIdx.x / p.split, step = (int)gridDim.x / p.split;   // this cluster's tiles
   const int kb0 = (int)((int64_t)rank * p.kbs / p.split), kb1 = (int)((int64_t)(rank + 1) * p.kbs / p.split);
   // acc[4 j + 2 h + i]: columns 8 j + 2 (lane % 4), +1 of the warp's, output 16 h + 8 i + lane / 4 of its 32
-  float2 acc[8 * NC];
+  uint64_t acc[8 * NC];
 
   if (warp == PRODUCER_WARP) {
     int n = 0;
     bool ok = true;
-    const uint32_t bytes = (uint32_t)(W_BYTES + p.cols * KB);
+    const uint32_t bytes = (uint32_t)((p.bn + p.cols) * KB);
     for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const int n0 = tile / p.n_mt * TILE_N, m0 = tile % p.n_mt * p.cols;
+      const int n0 = tile * p.bn;
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
         const int stage = n % S::NSTAGE, round = n / S::NSTAGE;
         if (round > 0) ok = wait_all(&empty[stage], (round - 1) & 1, abort_flag, p.status);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
           const uint32_t dst = saddr(sm + stage * S::STAGE);
           mbar_expect_tx(&full[stage], bytes);
           tma_load_2d(dst, &tmap_w, kb * KB, n0, &full[stage]);
-          tma_load_2d(dst + W_BYTES, &tmap_a, kb * KB, m0, &full[stage]);
+          tma_load_2d(dst + W_BYTES, &tmap_a, kb * KB, 0, &full[stage]);
         }
         __syncwarp();
       }
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     volatile int dummy = 0;
     mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
   } else if (warp == SCALE_WARP) {
-    // slot: [SG][COLS] scales of the tile's rows of a, then (ROWS1) [SG][128] scales of its weight rows
+    // slot: [SG][COLS] scales of the rows of a, then [SG][128] scales of the tile's weight rows
     int n = 0;
     bool ok = true;
     // the scales of blocks kb .. kb + 3 of one row (blocks past kb1 and rows past the last: 0)
@@ -220,18 +220,16 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       }
     };
     for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const int nt = tile / p.n_mt, m0 = tile % p.n_mt * p.cols;
       for (int kb = kb0; kb < kb1; kb += SG, ++n) {
-        float v[2 * NC][SG], w[4][SG], b[SG] = {1.f, 1.f, 1.f, 1.f};
+        float v[2 * NC][SG], w[4][SG];
         // all of the slot's loads in flight before the wait for its release
 #pragma unroll
         for (int i = 0; i < 2 * NC; ++i)
-          if (32 * i < p.cols) load4(p.sa, m0 + 32 * i + lane, p.M, kb, v[i]);
-        if (ROWS1) {
+          if (32 * i < p.cols) load4(p.sa, 32 * i + lane, p.M, kb, v[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load4(p.sw, (int64_t)nt * TILE_N + 32 * i + lane, p.N, kb, w[i]);
-        } else {
-          load4(p.sw, nt, nt + 1, kb, b);
+        for (int i = 0; i < 4; ++i) {
+          const int64_t row = (int64_t)tile * p.bn + 32 * i + lane;
+          load4(p.sw, p.w_rows == 1 ? row : row >> 7, p.w_rows == 1 ? p.N : ((int64_t)p.N + 127) >> 7, kb, w[i]);
         }
         const int slot = n % NSLOT, round = n / NSLOT;
         if (round > 0) ok = wait_all(&s_empty[slot], (round - 1) & 1, abort_flag, p.status);
@@ -241,12 +239,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         for (int i = 0; i < 2 * NC; ++i)
           if (32 * i < p.cols)
 #pragma unroll
-            for (int j = 0; j < SG; ++j) dst[j * S::COLS + 32 * i + lane] = ROWS1 ? v[i][j] : v[i][j] * b[j];
-        if (ROWS1)
+            for (int j = 0; j < SG; ++j) dst[j * S::COLS + 32 * i + lane] = v[i][j];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < SG; ++j) dst[SG * S::COLS + j * TILE_N + 32 * i + lane] = w[i][j];
+          for (int j = 0; j < SG; ++j) dst[SG * S::COLS + j * TILE_N + 32 * i + lane] = w[i][j];
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_full[slot]);
       }
@@ -259,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step) {
 #pragma unroll
-      for (int i = 0; i < 8 * NC; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < 8 * NC; ++i) acc[i] = 0ull;
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
         const int slot = ns % NSLOT, j = (kb - kb0) % SG;
         if (j == 0) ok = wait_all(&s_full[slot], (ns / NSLOT) & 1, abort_flag, p.status);
@@ -268,12 +265,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         if (!ok) break;
         tc_fence_after();
         const float* sc = scales + slot * S::SLOT_FLOATS + j * S::COLS + c0 + fc;
-        float rw[4] = {1.f, 1.f, 1.f, 1.f};                        // the weight scales of the thread's four outputs
-        if (ROWS1) {
-          const float* sr = scales + slot * S::SLOT_FLOATS + SG * S::COLS + j * TILE_N + quarter * 32 + fr;
+        uint64_t rw[4];                                            // the weight scales of the thread's four outputs, twice each
+        const float* sr = scales + slot * S::SLOT_FLOATS + SG * S::COLS + j * TILE_N + quarter * 32 + fr;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) rw[i] = sr[8 * i];
-        }
+        for (int i = 0; i < 4; ++i) rw[i] = pack2(make_float2(sr[8 * i], sr[8 * i]));
         const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * S::COLS + c0);
 #pragma unroll
         for (int c = 0; c < 16 * NC; c += 32) {                    // 32 columns at a time, 16 at an odd end
@@ -293,13 +288,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
           }
 #pragma unroll
           for (int g = 0; g < w / 8; ++g) {
-            const float2 s = *(const float2*)(sc + c + 8 * g);
+            const uint64_t s = *(const uint64_t*)(sc + c + 8 * g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float2& q = acc[4 * (c / 8 + g) + i];
+              uint64_t& q = acc[4 * (c / 8 + g) + i];
               const uint32_t* v = t[i >> 1] + 4 * g + 2 * (i & 1);
-              q.x = fmaf(__uint_as_float(v[0]), ROWS1 ? s.x * rw[i] : s.x, q.x);
-              q.y = fmaf(__uint_as_float(v[1]), ROWS1 ? s.y * rw[i] : s.y, q.y);
+              q = fma2(pack2(v[0], v[1]), mul2(s, rw[i]), q);
             }
           }
         }
@@ -315,22 +309,23 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       }
       if (!ok || p.split > 1) break;
       // eight columns at a time through the warp's own shared memory, so that a store covers 32 consecutive outputs
-      const int64_t n_out = (int64_t)(tile / p.n_mt) * TILE_N + quarter * 32 + lane;
-      const int m0 = tile % p.n_mt * p.cols + c0;
-      const int m_cols = min(mine, p.M - m0);
+      const int o = quarter * 32 + lane;
+      const int64_t n_out = (int64_t)tile * p.bn + o;
+      const bool mine_out = o < p.bn && n_out < p.N;
+      const int m_cols = min(mine, p.M - c0);
       float* tr = (float*)(sm + S::OFF_TR) + warp * TR_FLOATS;
-      int64_t off = (int64_t)m0 * p.ld_out + n_out;
+      int64_t off = (int64_t)c0 * p.ld_out + n_out;
 #pragma unroll
       for (int g = 0; g < 2 * NC; ++g) {
         if (8 * g >= m_cols) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = acc[4 * g + i];
+          const float2 v = unpack2(acc[4 * g + i]);
           tr[fc * TR_LD + 8 * i + fr] = v.x;
           tr[(fc + 1) * TR_LD + 8 * i + fr] = v.y;
         }
         __syncwarp();
-        if (n_out < p.N) {
+        if (mine_out) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (8 * g + e < m_cols) store_out(p, off + e * p.ld_out, tr[e * TR_LD + lane]);
@@ -353,28 +348,32 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       for (int g = 0; g < 2 * NC; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = acc[4 * g + i];
+          const float2 v = unpack2(acc[4 * g + i]);
           part[(c0 + 8 * g) * PAD_N + o + 8 * i] = v.x;
           part[(c0 + 8 * g + 1) * PAD_N + o + 8 * i] = v.y;
         }
     }
     cluster_sync();
     if (warp < EPI_WARPS) {
-      const int tile = first;
-      const int m0 = tile % p.n_mt * p.cols, m_cols = min(p.cols, p.M - m0);
-      const int r0 = (int)((int64_t)rank * m_cols / p.split), r1 = (int)((int64_t)(rank + 1) * m_cols / p.split);
-      const int o = threadIdx.x & (TILE_N - 1);
-      const int64_t n_out = (int64_t)(tile / p.n_mt) * TILE_N + o;
-      for (int c = r0 + (threadIdx.x >> 7); c < r1; c += EPI_WARPS / 4) {
-        const uint32_t at = saddr(part + c * PAD_N + o);
-        float v[MAX_SPLIT];
+      const int r0 = rank * p.M / p.split, r1 = (rank + 1) * p.M / p.split;
+      const int o = 4 * lane;                              // this thread's four outputs of a column
+      const int n_first = first * p.bn, n_end = min(p.N, n_first + p.bn);
+      for (int c = r0 + warp; c < r1; c += EPI_WARPS) {
+        float4 v[MAX_SPLIT];                               // every remote read in flight at once
 #pragma unroll
-        for (int r = 0; r < MAX_SPLIT; ++r) v[r] = r < p.split ? ld_cluster(at, r) : 0.f;
-        float sum = v[0];
+        for (int r = 0; r < MAX_SPLIT; ++r)
+          v[r] = r < p.split ? ld_cluster4(saddr(part + c * PAD_N + o), r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 sum = v[0];
 #pragma unroll
         for (int r = 1; r < MAX_SPLIT; ++r)
-          if (r < p.split) sum += v[r];
-        if (n_out < p.N) store_out(p, (int64_t)(m0 + c) * p.ld_out + n_out, sum);
+          if (r < p.split) {
+            sum.x += v[r].x; sum.y += v[r].y; sum.z += v[r].z; sum.w += v[r].w;
+          }
+        const int64_t off = (int64_t)c * p.ld_out + n_first + o;
+        const float e[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n_first + o + i < n_end) store_out(p, off + i, e[i]);
       }
     }
     cluster_sync();                // no CTA leaves while another reads its shared memory
@@ -389,11 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Params);
 
-template <bool ROWS1>
-Kernel pick(int nc) {
-  return nc == 1 ? gemm_fp8_kernel<1, ROWS1> : gemm_fp8_kernel<2, ROWS1>;
-}
-
+Kernel pick(int nc) { return nc == 1 ? gemm_fp8_kernel<1> : gemm_fp8_kernel<2>; }
 int smem_bytes(int nc) { return nc == 1 ? Shape<1>::BYTES : Shape<2>::BYTES; }
 
 cudaLaunchConfig_t config(unsigned grid, int split, int nc, cudaStream_t st, cudaLaunchAttribute* attrs) {
@@ -426,7 +421,7 @@ int resident_clusters(int split) {
   int n = 0;
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = config((unsigned)split, split, 2, 0, attrs);
-  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel<2, false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel<2>, &cfg) != cudaSuccess) {
     cudaGetLastError();            // not a fault of the call: such clusters are not used
     n = 0;
   }
@@ -434,26 +429,37 @@ int resident_clusters(int split) {
   return n;
 }
 
-// CTAs per tile: the split of K with the shortest modelled time, in blocks: waves of tiles, each of
-// (its share of the blocks + the cost of starting, summing and storing a tile).
-int choose_split(int64_t tiles, int kbs) {
-  const double fixed = 6, join = 3;
-  int best = 1;
-  double best_t = 0;
+// The outputs of a tile and the CTAs per tile (a split of K) with the shortest modelled time, in cycles: waves of
+// tiles, each of its blocks (a block's four MMAs take 420; its operands arrive at the SM's share of the memory rate,
+// 23 bytes a cycle with every SM loading, 50 at most) and a fixed cost (start of the pipeline, store; with a split the
+// join through distributed shared memory).
+void choose_tiles(int64_t N, int cols, int kbs, int* bn, int* split) {
+  const double fixed = 3000, join = 2500;
+  *split = 0;
+  double best = 0;
   for (int s = 1; s <= MAX_SPLIT && s <= std::max(kbs, 1); ++s) {
     const int64_t at_once = resident_clusters(s);
     if (at_once < 1) continue;
-    const double t = (double)ceil_div(tiles, at_once) * ((double)ceil_div(kbs, s) + fixed + (s > 1 ? join : 0));
-    if (s == 1 || t < best_t) {
-      best = s;
-      best_t = t;
+    const int64_t w0 = ceil_div(ceil_div(N, TILE_N), at_once);             // waves of the widest tiles
+    for (int64_t w = w0; w <= w0 + 1; ++w) {
+      const int width = (int)std::min<int64_t>(TILE_N, std::max<int64_t>(ceil_div(ceil_div(N, at_once * w), 8) * 8, 32));
+      const int64_t tiles = ceil_div(N, width), waves = ceil_div(tiles, at_once);
+      const double rate = std::min(50.0, 23.0 * num_sms() / (double)(std::min(tiles, at_once) * s));
+      const double block = std::max(420.0, (double)(width + cols) * KB / rate);
+      const double t = (double)waves * ((double)ceil_div(kbs, s) * block + fixed + (s > 1 ? join : 0));
+      if (*split == 0 || t < best) {
+        best = t;
+        *split = s;
+        *bn = width;
+      }
     }
   }
-  return best;
 }
 
 }  // namespace gtc
 
+// Rows of a from which the pairs of CTAs take the call: 128 x 154880 x 6144 takes 182 us here and 218 there, and
+// this kernel's tile has at most 128 columns.
 constexpr int64_t kPairRows = 128;
 
 int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
@@ -462,13 +468,25 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
     set_error("gemm_fp8_block128: needs a GPU of compute capability 10.x");
     return MTPSD_EUNSUPPORTED;
   }
-  if (g.M > kPairRows && g.K > 0) return launch_gemm_fp8_pair(g, st);
+  if (g.K == 0) {                   // an empty sum
+    const size_t es = g.out_f32 ? 4 : 2;
+    cudaMemset2DAsync(g.out, (size_t)g.ld_out * es, 0, (size_t)g.N * es, (size_t)g.M, st);
+    return check_launch("gemm_fp8_block128");
+  }
+  if (g.M > kPairRows) return launch_gemm_fp8_pair(g, st);
   Params p;
   p.sa = g.a_scale; p.sw = g.w_scale; p.out = g.out; p.ld_out = g.ld_out;
   p.M = (int)g.M; p.N = (int)g.N; p.kbs = (int)(g.K / KB);
-  p.n_mt = (int)ceil_div(g.M, 128);
-  p.cols = (int)(ceil_div(ceil_div(g.M, p.n_mt), 16) * 16);
-  const int64_t tiles = ceil_div(g.N, TILE_N) * p.n_mt;
+  p.cols = (int)(ceil_div(g.M, 16) * 16);
+  p.w_rows = g.w_scale_rows;
+  const int nc = (p.cols + 63) / 64;
+  static std::atomic<uint64_t> attr[2];
+  if (!set_smem_limit_once(pick(1), smem_bytes(1), attr[0]) || !set_smem_limit_once(pick(2), smem_bytes(2), attr[1])) {
+    set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
+    return MTPSD_ECUDA;
+  }
+  choose_tiles(g.N, p.cols, p.kbs, &p.bn, &p.split);
+  const int64_t tiles = ceil_div(g.N, p.bn);
   if (tiles > 0x3fffffffLL / MAX_SPLIT) {
     set_error("gemm_fp8_block128: too many output tiles");
     return MTPSD_EUNSUPPORTED;
@@ -477,28 +495,16 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   p.out_f32 = g.out_f32;
   p.vec_scales = p.kbs % 4 == 0 && (uintptr_t)g.a_scale % 16 == 0 && (uintptr_t)g.w_scale % 16 == 0;
   p.status = g.status;
-  const int nc = (p.cols + 63) / 64;
   CUtensorMap mw, ma;
-  memset(&mw, 0, sizeof(mw));
-  memset(&ma, 0, sizeof(ma));
-  if (p.kbs > 0 && (!make_tma_2d(&mw, 0, g.w, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, KB, TILE_N, true) ||
-                    !make_tma_2d(&ma, 0, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, KB, (uint32_t)p.cols, true))) {
+  if (!make_tma_2d(&mw, 0, g.w, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, KB, (uint32_t)p.bn, true) ||
+                    !make_tma_2d(&ma, 0, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, KB, (uint32_t)p.cols, true)) {
     set_error("gemm_fp8_block128: cuTensorMapEncodeTiled failed");
     return MTPSD_ECUDA;
   }
-  const bool rows1 = g.w_scale_rows == 1;
-  Kernel kern = rows1 ? pick<true>(nc) : pick<false>(nc);
-  static std::atomic<uint64_t> attr[4], attr2;
-  if (!set_smem_limit_once(kern, smem_bytes(nc), attr[(rows1 ? 2 : 0) + nc - 1]) ||
-      !set_smem_limit_once(gemm_fp8_kernel<2, false>, smem_bytes(2), attr2)) {
-    set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
-    return MTPSD_ECUDA;
-  }
-  p.split = choose_split(p.tiles, p.kbs);
   const unsigned grid = p.split > 1 ? (unsigned)(p.tiles * p.split) : (unsigned)std::min<int64_t>(p.tiles, num_sms());
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = config(grid, p.split, nc, st, attrs);
-  cudaLaunchKernelEx(&cfg, kern, mw, ma, p);
+  cudaLaunchKernelEx(&cfg, pick(nc), mw, ma, p);
   return check_launch("gemm_fp8_block128");
 }
 

@@ -1,9 +1,10 @@
 // FP8 product with block-128 scales for many rows: the arithmetic of
 // k_gemm_fp8.cu on pairs of CTAs (tcgen05.mma cta_group::2).
 //
-// A tile is 256 rows of a (operand A, M = 256, 128 per CTA) x 256 outputs
-// (operand B, N = 256): each CTA of the pair stages its 128 rows of a and 128
-// of the 256 weight rows, and the two tensor cores share both halves of B.  Per
+// A tile is 256 rows of a (operand A, M = 256, 128 per CTA) x 64 NP outputs
+// (operand B, N = 128, 192 or 256, chosen so that the tiles fill the last wave):
+// each CTA of the pair stages its 128 rows of a and half of the weight rows, and
+// the two tensor cores share both halves of B.  With N = 256, per
 // block a CTA moves 32 KB through shared memory for 4.2 M products, against 48
 // KB for a 128 x 256 tile of its own: at the full MMA rate (512 cycles a block)
 // the TMA writes and the operand reads then take 256 cycles each of the
@@ -12,14 +13,15 @@
 // thread multiplies by one scale per lane and block, without a read per column.
 //
 // Roles (384 threads, one CTA per SM), as k_gemm_fp8.cu but:
-//   warps 0-7   epilogue: lanes 32 (w % 4) .. +31, columns 128 (w / 4) .. +127; 128 accumulators a thread
-//               (setmaxnreg moves the other warps' registers here: 208 against 88).
+//   warps 0-7   epilogue: lanes 32 (w % 4) .. +31, of every 64 columns the 32 of half w / 4; 32 NP
+//               accumulators a thread (setmaxnreg moves the other warps' registers here: 200 against 104).
+//               Sixteen warps of half as many were slower (697 against 601 us at 768 x 154880 x 6144): a
+//               warp's waits and hand-offs cost about 130 instructions a block, whatever it adds.
 //   warp 8      TMA producer of this CTA's operands; both CTAs' copies complete on the leader's barrier.
 //   warp 9      TMEM allocation; in the leader (even) CTA the MMA issue for the pair.
 //   warp 10     scales of this CTA's rows of a;  warp 11  scales of the tile's weight rows.
 // With few tiles the blocks of K are split over up to 4 pairs of one cluster.
 #include <algorithm>
-#include <string.h>
 
 #include "gemm_fp8.cuh"
 
@@ -28,7 +30,9 @@ namespace gtp {
 using namespace gtc;
 
 constexpr int ROWS = 128;                 // rows of a per CTA, weight rows per CTA
-constexpr int COLS = 256;                 // outputs of a tile
+constexpr int COLS = 256;                 // most outputs of a tile
+constexpr int RUNS = COLS / 64;           // runs of 64 outputs: each lies in one 128 x 128 weight block
+constexpr int PW = 2;                     // 16-column pieces of a run of 64 per epilogue warp
 constexpr int EPI_WARPS = 8;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, SCALE_WARP = 10;
 constexpr int THREADS = 32 * 12;
@@ -38,10 +42,8 @@ constexpr int STAGE = 2 * HALF_BYTES;
 constexpr int NSTAGE = 6;
 constexpr int NBUF = TMEM_COLS / COLS;
 constexpr int SLOT_FLOATS = SG * (ROWS + COLS);
-constexpr int TR_LD = 40;                 // row stride (floats) of 8 rows x 32 columns: fragment rows miss each other's banks
-constexpr int TR_LD_BF16 = 36;            // the same in words of two bf16, 8 rows x 64 columns
-constexpr int TR_LD_ROWS = 17;            // the same for 32 rows x 16 columns of the one-row-per-thread layout
-constexpr int TR_FLOATS = 640;            // per epilogue warp
+constexpr int TR_LD = 9;                  // row stride (floats) of the transposed store of 32 rows x 8 columns
+constexpr int TR_FLOATS = 32 * TR_LD;     // per epilogue warp
 constexpr int PART_LD = COLS + 8;         // row stride of a partial tile
 constexpr int OFF_SCALE = NSTAGE * STAGE;
 constexpr int OFF_TR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;
@@ -49,10 +51,9 @@ constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
 constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + alignment slack
-constexpr int EPI_REGS = 208, ROLE_REGS = 88;
+constexpr int EPI_REGS = 200, ROLE_REGS = 104;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 static_assert(ROWS * PART_LD * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
-static_assert(8 * TR_LD <= TR_FLOATS && 8 * TR_LD_BF16 <= TR_FLOATS && 32 * TR_LD_ROWS <= TR_FLOATS, "the transposes fit");
 // setmaxnreg shares out what the launch allots: 65536 / 384 threads, rounded down to 8
 static_assert(256 * EPI_REGS + 128 * ROLE_REGS <= THREADS * 168, "register split");
 
@@ -65,7 +66,6 @@ struct Params {
   int n_mt, tiles;        // tiles along M, tiles
   int split;              // pairs per cluster
   int out_f32;
-  int vec_out;            // bf16 outputs can be stored in pairs
   int vec_rows;           // a row's outputs can be stored 32 bytes at a time
   int vec_scales;         // a block row's scales can be read four at a time
   int32_t* status;
@@ -112,8 +112,8 @@ __device__ __forceinline__ bool wait_all_cluster(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar::wait<true>(bar, parity, abort_flag, status, mbar::DEFAULT_LIMIT_NS));
 }
 
-// ROWS1: the weight's scales are per row and block (else per 128 x 128 block).
-template <bool ROWS1>
+// NP: a tile has 64 NP outputs.  ROWS1: the weight's scales are per row and block (else per 128 x 128 block).
+template <int NP, bool ROWS1>
 __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_w,
                                                                    const __grid_constant__ CUtensorMap tmap_a,
                                                                    const __grid_constant__ Params p) {
@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
   volatile int* abort_flag = (volatile int*)(sm + OFF_MISC + 4);
   float* scales = (float*)(sm + OFF_SCALE);
 
+  constexpr int BN = 64 * NP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), leader = crank & ~1u, side = crank & 1u;
   if (threadIdx.x == 0) {
@@ -177,13 +178,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
       int stage = 0, n = 0;
       bool ok = true;
       for (int tile = first; tile < p.tiles && ok; tile += step) {
-        const int n0 = tile / p.n_mt * COLS + (int)side * ROWS, m0 = (tile % p.n_mt * 2 + (int)side) * ROWS;
+        const int n0 = tile / p.n_mt * BN + (int)side * (BN / 2), m0 = (tile % p.n_mt * 2 + (int)side) * ROWS;
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
           if (n >= NSTAGE) ok = wait_all(&empty[stage], (n / NSTAGE - 1) & 1, abort_flag, p.status);
           if (!ok) break;
           if (elect_one()) {
             const uint32_t dst = saddr(sm + stage * STAGE), bar = map_rank(saddr(&full[stage]), leader);
-            if (side == 0) mbar_expect_tx(&full[stage], 2 * STAGE);    // both CTAs' copies
+            if (side == 0) mbar_expect_tx(&full[stage], 2u * HALF_BYTES + (uint32_t)(BN * KB));    // both CTAs' copies
             tma_load_pair(dst, &tmap_a, kb * KB, m0, bar);
             tma_load_pair(dst + HALF_BYTES, &tmap_w, kb * KB, n0, bar);
           }
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
     } else if (warp == MMA_WARP && side == 0) {
       int stage = 0, n = 0;
       bool ok = true;
-      const uint32_t id = (1u << 4) | ((uint32_t)COLS >> 3 << 17) | ((256u >> 4) << 24);   // M = 256, N = 256
+      const uint32_t id = (1u << 4) | ((uint32_t)BN >> 3 << 17) | ((256u >> 4) << 24);   // M = 256, N = BN
       const uint32_t mask = 3u << leader;
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
@@ -229,18 +230,17 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
       mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
     } else if (warp >= SCALE_WARP) {
       // slot: [SG][128] scales of this CTA's rows of a, then [SG][256] of the tile's weight rows (ROWS1) or
-      // [SG][2] of its two blocks
+      // [SG][4] of the blocks of its runs of 64
       const bool rows = warp == SCALE_WARP;
       int n = 0;
       bool ok = true;
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const int nt = tile / p.n_mt;
         const float* base = rows ? p.sa : p.sw;
-        const int64_t row0 = rows ? (int64_t)(tile % p.n_mt * 2 + (int)side) * ROWS
-                                  : ROWS1 ? (int64_t)nt * COLS : (int64_t)nt * (COLS / 128);
-        const int64_t end = rows ? p.M : ROWS1 ? p.N : ((int64_t)p.N + 127) / 128;
-        const int per = rows ? ROWS : ROWS1 ? COLS : 2;             // scales per block
-        const int ld = rows ? ROWS : ROWS1 ? COLS : 2;
+        const int64_t row0 = rows ? (int64_t)(tile % p.n_mt * 2 + (int)side) * ROWS : (int64_t)nt * BN;
+        const int64_t end = rows ? p.M : p.N;
+        const int per = rows ? ROWS : ROWS1 ? BN : NP;      // scales per block
+        const int ld = rows ? ROWS : ROWS1 ? COLS : RUNS;
         for (int kb = kb0; kb < kb1; kb += SG, ++n) {
           const int slot = n % NSLOT;
           float* dst = scales + slot * SLOT_FLOATS + (rows ? 0 : SG * ROWS);
@@ -251,8 +251,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
             for (int i = 0; i < 4; ++i) {         // blocks past kb1 and rows past the last: 0
               const int at = i0 + 32 * i + lane;
               v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-              if (at >= per || row0 + at >= end) continue;
-              const float* s = base + (row0 + at) * p.kbs + kb;
+              int64_t row = row0 + (rows || ROWS1 ? at : 64 * at);
+              if (at >= per || row >= end) continue;
+              if (!rows && !ROWS1) row >>= 7;
+              const float* s = base + row * p.kbs + kb;
               if (p.vec_scales && (kb & 3) == 0) {
                 const float4 f = __ldg((const float4*)s);
                 v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
@@ -288,12 +290,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
   }
 
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
-  const int quarter = warp & 3, c0 = (warp >> 2) * 128;            // this warp's TMEM lanes and first column
+  const int quarter = warp & 3, c0 = 16 * PW * (warp >> 2);        // this warp's TMEM lanes and columns 64 r + c0 .. +31
   const int fr = lane >> 2, fc = 2 * (lane & 3);                   // fragment row and column of this lane
-  // ROWS1: acc[4 g + i]: columns c0 + 8 g + fc, +1, row 32 quarter + 8 i + fr (the 16x256b read of k_gemm_fp8.cu);
-  // else acc[i]: columns c0 + 2 i, +1, row 32 quarter + lane (the 32x32b read, twice as fast: 128 x 256 values
-  // take 306 cycles, against 612 which the additions then cannot hide)
-  float2 acc[64];
+  // Piece c holds the columns at(c) = 64 (c / PW) + 16 (c % PW) + c0 .. +15.  ROWS1: acc[8 c + 4 g + i]: columns
+  // at(c) + 8 g + fc, +1, row 32 quarter + 8 i + fr (the 16x256b read of k_gemm_fp8.cu); else acc[8 c + i]: columns
+  // at(c) + 2 i, +1, row 32 quarter + lane (the 32x32b read, twice as fast: 768 x 154880 x 6144 took 855 us with the other)
+  uint64_t acc[8 * NP * PW];
   {
     int buf = 0, t_phase = 0, slot = 0, s_phase = 0;
     bool ok = true;
@@ -303,39 +305,42 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
       const int m_own = (tile % p.n_mt * 2 + (int)side) * ROWS + quarter * 32;    // the warp's first row of a
       const bool live = m_own < p.M;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < 8 * NP * PW; ++i) acc[i] = 0ull;
       for (int kb = kb0, j = 0; kb < kb1; ++kb) {
         if (j == 0) ok = wait_all(&s_full[slot], s_phase, abort_flag, p.status);
         if (!ok) break;
-        const float* sc = scales + slot * SLOT_FLOATS;
-        float rs[4];                                               // the scales of the thread's rows
-        if (ROWS1) {
+        // every scale is read before the wait for the products: the chain of a block is what bounds this loop
+        const float* sc = scales + slot * SLOT_FLOATS + j * ROWS + quarter * 32;
+        const float* scw = scales + slot * SLOT_FLOATS + SG * ROWS + j * (ROWS1 ? COLS : RUNS);
+        float rs[4], ws[4];
+        if constexpr (ROWS1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) rs[i] = sc[j * ROWS + quarter * 32 + 8 * i + fr];
+          for (int i = 0; i < 4; ++i) rs[i] = sc[8 * i + fr];
         } else {
-          rs[0] = sc[j * ROWS + quarter * 32 + lane] * sc[SG * ROWS + 2 * j + (c0 >> 7)];
+          const float4 w = *(const float4*)scw;
+          const float r = sc[lane];
+          ws[0] = r * w.x; ws[1] = r * w.y; ws[2] = r * w.z; ws[3] = r * w.w;
         }
-        const float* scw = sc + SG * ROWS + j * COLS + c0 + fc;
         ok = wait_all(&t_full[buf], t_phase, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = taddr0 + (uint32_t)(buf * COLS);
         if (live) {
-          // 32 columns x 32 lanes at a time; the next read is in flight while one is added
-          uint32_t t[2][32];
+          // 16 columns x 32 lanes at a time; the next read is in flight while one is added
+          uint32_t t[2][16];
           auto read = [&](int c) {
             if constexpr (ROWS1) {
-              tmem_ld_x4(taddr + 32 * c, t[c & 1]);
-              tmem_ld_x4(taddr + (16u << 16) + 32 * c, t[c & 1] + 16);
+              tmem_ld_x2(taddr + 64 * (c / PW) + 16 * (c % PW), t[c & 1]);
+              tmem_ld_x2(taddr + (16u << 16) + 64 * (c / PW) + 16 * (c % PW), t[c & 1] + 8);
             } else {
-              tmem_ld_rows32(taddr + 32 * c, t[c & 1]);
+              tmem_ld_rows16(taddr + 64 * (c / PW) + 16 * (c % PW), t[c & 1]);
             }
           };
           read(0);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < NP * PW; ++c) {
             tmem_ld_wait();
-            if (c < 3) {
+            if (c + 1 < NP * PW) {
               read(c + 1);
             } else {               // the warp's last read of the buffer
               tc_fence_before();
@@ -344,23 +349,19 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
             }
             if constexpr (ROWS1) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float2 s = *(const float2*)(scw + 32 * c + 8 * g);
+              for (int g = 0; g < 2; ++g) {
+                const uint64_t s = *(const uint64_t*)(scw + 64 * (c / PW) + 16 * (c % PW) + c0 + 8 * g + fc);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  float2& q = acc[4 * (4 * c + g) + i];
-                  const uint32_t* v = t[c & 1] + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
-                  q.x = fmaf(__uint_as_float(v[0]), rs[i] * s.x, q.x);
-                  q.y = fmaf(__uint_as_float(v[1]), rs[i] * s.y, q.y);
+                  uint64_t& q = acc[8 * c + 4 * g + i];
+                  const uint32_t* v = t[c & 1] + 8 * (i >> 1) + 4 * g + 2 * (i & 1);
+                  q = fma2(pack2(v[0], v[1]), mul2(s, pack2(make_float2(rs[i], rs[i]))), q);
                 }
               }
             } else {
+              const uint64_t s = pack2(make_float2(ws[c / PW], ws[c / PW]));
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float2& q = acc[16 * c + i];
-                q.x = fmaf(__uint_as_float(t[c & 1][2 * i]), rs[0], q.x);
-                q.y = fmaf(__uint_as_float(t[c & 1][2 * i + 1]), rs[0], q.y);
-              }
+              for (int i = 0; i < 8; ++i) acc[8 * c + i] = fma2(pack2(t[c & 1][2 * i], t[c & 1][2 * i + 1]), s, acc[8 * c + i]);
             }
           }
         } else {
@@ -383,93 +384,57 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
       }
       if (!ok || p.split > 1) break;
       if (!live) continue;
-      const int n_first = tile / p.n_mt * COLS + c0;
-      float* tr = (float*)(sm + OFF_TR) + warp * TR_FLOATS;
+      const int n_first = tile / p.n_mt * BN + c0;
       if constexpr (!ROWS1) {
-        const int es = p.out_f32 ? 4 : 2, row = m_own + lane;
-        uint8_t* o = (uint8_t*)p.out + ((int64_t)row * p.ld_out + n_first) * es;
-        if (p.vec_rows && n_first + 128 <= p.N) {           // 32 bytes of its own row per thread
+        if (p.vec_rows && tile / p.n_mt * BN + BN <= p.N) {          // 32 bytes of its own row per thread
+          const int es = p.out_f32 ? 4 : 2, row = m_own + lane;
+          uint8_t* o = (uint8_t*)p.out + ((int64_t)row * p.ld_out + n_first) * es;
           if (row < p.M) {
-            if (p.out_f32) {
 #pragma unroll
-              for (int i = 0; i < 64; i += 4) store_32b(o + 8 * i, (const uint32_t*)&acc[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 64; i += 8) {
+            for (int c = 0; c < NP * PW; ++c) {
+              const int at = 64 * (c / PW) + 16 * (c % PW);
+              if (p.out_f32) {
+                store_32b(o + 4 * at, (const uint32_t*)&acc[8 * c]);
+                store_32b(o + 4 * at + 32, (const uint32_t*)&acc[8 * c + 4]);
+              } else {
                 uint32_t v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = bf16_pair(acc[i + e]);
-                store_32b(o + 4 * i, v);
+                for (int e = 0; e < 8; ++e) v[e] = bf16_pair(unpack2(acc[8 * c + e]));
+                store_32b(o + 2 * at, v);
               }
             }
           }
-        } else {                   // through the warp's own shared memory, so that a store covers 16 consecutive outputs
-#pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            if (n_first + c >= p.N) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              tr[lane * TR_LD_ROWS + 2 * i] = acc[c / 2 + i].x;
-              tr[lane * TR_LD_ROWS + 2 * i + 1] = acc[c / 2 + i].y;
-            }
-            __syncwarp();
-            const int col = n_first + c + (lane & 15);
-            for (int r = lane >> 4; r < 32; r += 2) {
-              if (m_own + r >= p.M) break;
-              const float v = tr[r * TR_LD_ROWS + (lane & 15)];
-              const int64_t off = (int64_t)(m_own + r) * p.ld_out + col;
-              if (col >= p.N) continue;
-              if (p.out_f32) ((float*)p.out)[off] = v;
-              else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
-            }
-            __syncwarp();
-          }
+          continue;
         }
-        continue;
       }
-      // eight rows at a time through the warp's own shared memory, so that a store covers consecutive outputs
-      if (p.out_f32) {
+      // eight columns at a time through the warp's own shared memory, so that a store covers consecutive outputs
+      float* tr = (float*)(sm + OFF_TR) + warp * TR_FLOATS;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int c = 0; c < NP * PW; ++c)
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+        for (int g = 0; g < 2; ++g) {
+          const int col0 = n_first + 64 * (c / PW) + 16 * (c % PW) + 8 * g;
+          if (col0 >= p.N) break;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) *(float2*)(tr + fr * TR_LD + 8 * g + fc) = acc[4 * (c / 8 + g) + i];
-            __syncwarp();
-            const int col = n_first + c + lane;
-            float* o = (float*)p.out + (int64_t)(m_own + 8 * i) * p.ld_out + col;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (m_own + 8 * i + e < p.M && col < p.N) o[e * p.ld_out] = tr[e * TR_LD + lane];
-            __syncwarp();
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = unpack2(acc[8 * c + 4 * g + i]);
+            float* at = ROWS1 ? tr + (8 * i + fr) * TR_LD + fc : tr + lane * TR_LD + 2 * i;
+            at[0] = v.x;
+            at[1] = v.y;
           }
-      } else {
-        uint32_t* tw = (uint32_t*)tr;
+          __syncwarp();
+          const int col = col0 + (lane & 7);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 128; c += 64) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              tw[fr * TR_LD_BF16 + 4 * g + (lane & 3)] = bf16_pair(acc[4 * (c / 8 + g) + i]);
-            }
-            __syncwarp();
-            const int col = n_first + c + 2 * lane;
-            __nv_bfloat16* o = (__nv_bfloat16*)p.out + (int64_t)(m_own + 8 * i) * p.ld_out + col;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (m_own + 8 * i + e >= p.M) break;
-              const uint32_t w = tw[e * TR_LD_BF16 + lane];
-              if (p.vec_out && col + 1 < p.N) {
-                *(uint32_t*)(o + e * p.ld_out) = w;
-              } else {
-                if (col < p.N) ((uint16_t*)(o + e * p.ld_out))[0] = (uint16_t)w;
-                if (col + 1 < p.N) ((uint16_t*)(o + e * p.ld_out))[1] = (uint16_t)(w >> 16);
-              }
-            }
-            __syncwarp();
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            if (m_own + r >= p.M || col >= p.N) continue;
+            const float v = tr[r * TR_LD + (lane & 7)];
+            const int64_t off = (int64_t)(m_own + r) * p.ld_out + col;
+            if (p.out_f32) ((float*)p.out)[off] = v;
+            else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
           }
-      }
+          __syncwarp();
+        }
     }
   }
   __syncwarp();
@@ -477,65 +442,62 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
     // The cluster's one tile: every CTA's accumulators into its own stage ring (the last block's MMAs are
     // done, so no copy or MMA uses it), then each pair sums a part of the rows over the pairs, in order.
     float* part = (float*)sm;                               // [128][PART_LD]
-    if constexpr (ROWS1) {
 #pragma unroll
-      for (int g = 0; g < 16; ++g)
+    for (int c = 0; c < NP * PW; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *(float2*)(part + (quarter * 32 + 8 * i + fr) * PART_LD + c0 + 8 * g + fc) = acc[4 * g + i];
-    } else {
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int i = 0; i < 64; i += 2)
-        *(float4*)(part + (quarter * 32 + lane) * PART_LD + c0 + 2 * i) = make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
-    }
+        for (int i = 0; i < 4; ++i) {
+          const int at = 64 * (c / PW) + 16 * (c % PW) + c0 + 8 * g;
+          *(uint64_t*)(ROWS1 ? part + (quarter * 32 + 8 * i + fr) * PART_LD + at + fc
+                             : part + (quarter * 32 + lane) * PART_LD + at + 2 * i) = acc[8 * c + 4 * g + i];
+        }
     cluster_sync();                // (1)
-    const int m_first = (first % p.n_mt * 2 + (int)side) * ROWS, n_first = first / p.n_mt * COLS;
+    const int m_first = (first % p.n_mt * 2 + (int)side) * ROWS, n_first = first / p.n_mt * BN;
+    const int n_end = min(p.N, n_first + BN);
     const int rows = min(ROWS, p.M - m_first);              // <= 0: this CTA's rows are past the last
     const int r0 = rows > 0 ? part_rank * rows / p.split : 0, r1 = rows > 0 ? (part_rank + 1) * rows / p.split : 0;
-    for (int r = r0 + warp; r < r1; r += EPI_WARPS) {
-      // a row's 256 outputs: columns 4 lane .. +3 and 128 + 4 lane .. +3, every remote read in flight at once
-      float4 v[MAX_SPLIT][2];
+    for (int r = r0 + (warp >> 1); r < r1; r += EPI_WARPS / 2) {
+      // half a row per warp, four columns per thread, every remote read in flight at once (columns past the
+      // tile's are read too, inside the partial tile, and dropped)
+      const int at = 128 * (warp & 1) + 4 * lane;
+      float4 v[MAX_SPLIT];
 #pragma unroll
       for (int q = 0; q < MAX_SPLIT; ++q)
+        v[q] = q < p.split ? ld_cluster4(saddr(part + r * PART_LD + at), 2 * q + side) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 sum = v[0];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v[q][h] = q < p.split ? ld_cluster4(saddr(part + r * PART_LD + 128 * h + 4 * lane), 2 * q + side)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4 sum = v[0][h];
-#pragma unroll
-        for (int q = 1; q < MAX_SPLIT; ++q)
-          if (q < p.split) {
-            sum.x += v[q][h].x; sum.y += v[q][h].y; sum.z += v[q][h].z; sum.w += v[q][h].w;
-          }
-        const int col = n_first + 128 * h + 4 * lane;
-        const int64_t off = (int64_t)(m_first + r) * p.ld_out + col;
-        const float e[4] = {sum.x, sum.y, sum.z, sum.w};
-        if (p.out_f32) {
-          if (p.vec_rows && col + 3 < p.N) {
-            *(float4*)((float*)p.out + off) = sum;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + i < p.N) ((float*)p.out)[off + i] = e[i];
-          }
-        } else {
-          if (p.vec_rows && col + 3 < p.N) {
-            *(uint2*)((__nv_bfloat16*)p.out + off) =
-                make_uint2(bf16_pair(make_float2(sum.x, sum.y)), bf16_pair(make_float2(sum.z, sum.w)));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + i < p.N) ((__nv_bfloat16*)p.out)[off + i] = __float2bfloat16_rn(e[i]);
-          }
+      for (int q = 1; q < MAX_SPLIT; ++q)
+        if (q < p.split) {
+          sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w;
         }
+      const int col = n_first + at;
+      const int64_t off = (int64_t)(m_first + r) * p.ld_out + col;
+      if (p.vec_rows && col + 3 < n_end) {
+        if (p.out_f32) *(float4*)((float*)p.out + off) = sum;
+        else *(uint2*)((__nv_bfloat16*)p.out + off) =
+            make_uint2(bf16_pair(make_float2(sum.x, sum.y)), bf16_pair(make_float2(sum.z, sum.w)));
+      } else {
+        const float e[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < n_end) {
+            if (p.out_f32) ((float*)p.out)[off + i] = e[i];
+            else ((__nv_bfloat16*)p.out)[off + i] = __float2bfloat16_rn(e[i]);
+          }
       }
     }
     __syncwarp();
   }
   tc_fence_before();
   cluster_sync();                  // (2)
+}
+
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Params);
+
+template <bool ROWS1>
+Kernel pick(int np) {
+  return np == 2 ? gemm_fp8_pair_kernel<2, ROWS1> : np == 3 ? gemm_fp8_pair_kernel<3, ROWS1> : gemm_fp8_pair_kernel<4, ROWS1>;
 }
 
 cudaLaunchConfig_t config(unsigned grid, int split, cudaStream_t st, cudaLaunchAttribute* attrs) {
@@ -567,7 +529,7 @@ int resident_clusters(int split) {
   int n = 0;
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = config(2u * split, split, 0, attrs);
-  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_pair_kernel<false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_pair_kernel<4, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();            // not a fault of the call: such clusters are not used
     n = 0;
   }
@@ -575,21 +537,26 @@ int resident_clusters(int split) {
   return n;
 }
 
-// Pairs per tile: the split of K with the shortest modelled time, in blocks (as k_gemm_fp8.cu).
-int choose_split(int64_t tiles, int kbs) {
-  const double fixed = 6, join = 3;
-  int best = 0;
-  double best_t = 0;
+// The tile width (64 np) and the pairs per tile (a split of K) with the shortest modelled time: waves of tiles, each of
+// its blocks (cycles per block measured at 256 outputs: 940, of which about 200 do not depend on the width) and a fixed cost
+// (start of the pipeline, store; with a split the join through distributed shared memory).
+void choose_tiles(int64_t N, int n_mt, int kbs, int* np, int* split) {
+  const double fixed = 5000, join = 5000;
+  *split = 0;
+  double best = 0;
   for (int s = 1; s <= MAX_SPLIT && s <= std::max(kbs, 1); ++s) {
     const int64_t at_once = resident_clusters(s);
     if (at_once < 1) continue;
-    const double t = (double)ceil_div(tiles, at_once) * ((double)ceil_div(kbs, s) + fixed + (s > 1 ? join : 0));
-    if (best == 0 || t < best_t) {
-      best = s;
-      best_t = t;
+    for (int w = 4; w >= 2; --w) {
+      const int64_t waves = ceil_div(ceil_div(N, 64 * w) * n_mt, at_once);
+      const double t = (double)waves * ((double)ceil_div(kbs, s) * (200 + 185 * w) + fixed + (s > 1 ? join : 0));
+      if (*split == 0 || t < best) {
+        best = t;
+        *split = s;
+        *np = w;
+      }
     }
   }
-  return best;
 }
 
 }  // namespace gtp
@@ -600,39 +567,43 @@ int launch_gemm_fp8_pair(const GemmFp8Plan& g, cudaStream_t st) {
   p.sa = g.a_scale; p.sw = g.w_scale; p.out = g.out; p.ld_out = g.ld_out;
   p.M = (int)g.M; p.N = (int)g.N; p.kbs = (int)(g.K / KB);
   p.n_mt = (int)ceil_div(g.M, 2 * ROWS);
-  const int64_t tiles = ceil_div(g.N, COLS) * p.n_mt;
+  const bool rows1 = g.w_scale_rows == 1;
+  static std::atomic<uint64_t> attr[2][5];
+  if (!set_smem_limit_once(pick<false>(4), SMEM_BYTES, attr[0][4])) {     // before the occupancy is asked for
+    set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
+    return MTPSD_ECUDA;
+  }
+  int np = 4;
+  choose_tiles(g.N, p.n_mt, p.kbs, &np, &p.split);
+  if (p.split < 1) {
+    set_error("gemm_fp8_block128: no pair of CTAs fits the device");
+    return MTPSD_EUNSUPPORTED;
+  }
+  const int64_t tiles = ceil_div(g.N, 64 * np) * p.n_mt;
   if (tiles > 0x3fffffffLL / (2 * MAX_SPLIT)) {
     set_error("gemm_fp8_block128: too many output tiles");
     return MTPSD_EUNSUPPORTED;
   }
   p.tiles = (int)tiles;
   p.out_f32 = g.out_f32;
-  p.vec_out = !g.out_f32 && g.ld_out % 2 == 0 && (uintptr_t)g.out % 4 == 0;
   p.vec_rows = g.ld_out * (g.out_f32 ? 4 : 2) % 32 == 0 && (uintptr_t)g.out % 32 == 0;
   p.vec_scales = p.kbs % 4 == 0 && (uintptr_t)g.a_scale % 16 == 0 && (uintptr_t)g.w_scale % 16 == 0;
   p.status = g.status;
   CUtensorMap mw, ma;
-  if (!make_tma_2d(&mw, 0, g.w, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, KB, ROWS, true) ||
+  if (!make_tma_2d(&mw, 0, g.w, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, KB, (uint32_t)(32 * np), true) ||
       !make_tma_2d(&ma, 0, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, KB, ROWS, true)) {
     set_error("gemm_fp8_block128: cuTensorMapEncodeTiled failed");
     return MTPSD_ECUDA;
   }
-  static std::atomic<uint64_t> attr[2];
-  if (!set_smem_limit_once(gemm_fp8_pair_kernel<false>, SMEM_BYTES, attr[0]) ||
-      !set_smem_limit_once(gemm_fp8_pair_kernel<true>, SMEM_BYTES, attr[1])) {
+  Kernel kern = rows1 ? pick<true>(np) : pick<false>(np);
+  if (!set_smem_limit_once(kern, SMEM_BYTES, attr[rows1][np])) {
     set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
-  }
-  p.split = choose_split(p.tiles, p.kbs);
-  if (p.split < 1) {
-    set_error("gemm_fp8_block128: no pair of CTAs fits the device");
-    return MTPSD_EUNSUPPORTED;
   }
   const int64_t clusters = p.split > 1 ? p.tiles : std::min<int64_t>(p.tiles, resident_clusters(1));
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = config((unsigned)(clusters * 2 * p.split), p.split, st, attrs);
-  if (g.w_scale_rows == 1) cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<true>, mw, ma, p);
-  else cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<false>, mw, ma, p);
+  cudaLaunchKernelEx(&cfg, kern, mw, ma, p);
   return check_launch("gemm_fp8_block128");
 }
 
