@@ -450,8 +450,7 @@ int mtpsd_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* o
                              int32_t B, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
                              const int32_t* count_rows, int32_t* dev_status, void* stream) {
   g_err[0] = 0;
-  if (B < 0 || B > 65535 || S < 0 || S > 0xffffffffLL)
-    return fail(MTPSD_EINVAL, "token_counts_build: need 0 <= B <= 65535, 0 <= S < 2^32");
+  if (B < 0 || S < 0 || S > 0xffffffffLL) return fail(MTPSD_EINVAL, "token_counts_build: need B >= 0, 0 <= S < 2^32");
   if (B == 0) return MTPSD_OK;
   if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows != nullptr, "token_counts_build")) return rc;
   if (!offsets || (S > 0 && !tokens)) return fail(MTPSD_EINVAL, "token_counts_build: null pointer");

@@ -2,25 +2,28 @@
 // int16 word per (request, token), sign bit = in the prompt, low 15 bits = the
 // number of occurrences in the output, held at 32767.
 //
-// Build: one launch clears the rows; a second counts, a CTA per 4096 tokens of a
-// request.  Text repeats its tokens, so the CTA first gathers them in a hash table in
-// shared memory and adds each distinct token once (one global update per token took
-// 1162 us for 128 requests of 1024 .. 131072 tokens: the updates of a frequent token
-// queue up).  The updates are additions with a limit and bit sets: any order gives the
-// same table.  Bounded by writing and clearing the table and by the updates in L2.
+// Build: a CTA per request, range of the vocabulary and part of the request's tokens
+// keeps the range's counts (16 bits) and prompt bits in shared memory; the parts of a
+// range are one cluster, whose CTAs add up the counts through distributed shared memory
+// and write every word of the row once.  The tokens are read once per range, from L2.
+// Updates of the table itself are far slower: one per token took 1162 us for 128
+// requests of 1024 .. 131072 tokens, one per token and 4096 tokens (gathered in a hash
+// table first) 45 us, because the updates of a frequent token queue up.
 // Accept: one thread per token that the step has put out.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace mtpsd {
 
-constexpr int SLICE = 4096;                   // tokens of a CTA
-constexpr int SLOTS = 2 * SLICE;              // of its hash table
-constexpr uint32_t EMPTY = 0xffffffffu;       // no key: tokens are below 2^31 - 1
-constexpr int BUILD_THREADS = 512;
-constexpr int BUILD_SMEM = SLOTS * 8;
-constexpr int CLEAR_THREADS = 256;
-constexpr int CLEAR_VECS = 8;                 // 16-byte stores per thread
+constexpr int BUILD_THREADS = 1024;
+constexpr int MAX_RANGE = 100352;             // tokens of a range: 196 KB of counts, 12 KB of bits
+constexpr int MAX_PARTS = 8;
+// Counts are cut to the limit after every 32768 tokens, so that none passes 32767 + 32768 before
+constexpr int BLOCK = 32768;
+constexpr int build_smem(int range) { return range * 2 + range / 8; }
+static_assert(build_smem(MAX_RANGE) <= 232448 - 1024 && MAX_RANGE % 128 == 0, "shared memory per CTA");
 
 // Adds n occurrences to the 16-bit word t of a row, held at 32767.  The words are updated through the
 // aligned 32-bit word that holds two of them, by compare and swap, so that a count at its limit never
@@ -62,113 +65,106 @@ __device__ __forceinline__ int64_t own_table_row(const int32_t* rows, int b, int
   return row;
 }
 
-__global__ void __launch_bounds__(CLEAR_THREADS) token_counts_clear_kernel(int16_t* __restrict__ counts, int64_t ld,
-                                                                           int n_rows, const int32_t* __restrict__ rows,
-                                                                           int32_t* status) {
-  griddep_wait();                // the previous kernel's writes are visible from here on
-  griddep_launch_dependents();
-  const int64_t row = own_table_row(rows, blockIdx.y, n_rows, blockIdx.x == 0 ? status : nullptr);
-  if (row < 0) return;
-  int4* at = (int4*)(counts + row * ld);
-  const int64_t v0 = (int64_t)blockIdx.x * CLEAR_THREADS * CLEAR_VECS + threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < CLEAR_VECS; ++i)
-    if (v0 + i * CLEAR_THREADS < ld / 8) at[v0 + i * CLEAR_THREADS] = make_int4(0, 0, 0, 0);
+__device__ __forceinline__ uint4 ld_peer(const void* p, uint32_t rank) {
+  uint32_t a;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
+__device__ __forceinline__ uint32_t ld_peer_u8(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The two counts of a word, each cut to the limit.
+__device__ __forceinline__ uint32_t limit2(uint32_t w) { return min(w & 0xffffu, 0x7fffu) | min(w >> 16, 0x7fffu) << 16; }
 
-__global__ void __launch_bounds__(BUILD_THREADS) token_counts_build_kernel(
+__global__ void __launch_bounds__(BUILD_THREADS, 1) token_counts_build_kernel(
     const int64_t* __restrict__ tokens, int64_t S, const uint32_t* __restrict__ offsets,
-    const int64_t* __restrict__ n_prompt, int B, int64_t V, int16_t* __restrict__ counts, int64_t ld, int n_rows,
-    const int32_t* __restrict__ rows, int32_t* status) {
+    const int64_t* __restrict__ n_prompt, int64_t V, int16_t* __restrict__ counts, int64_t ld, int n_rows,
+    const int32_t* __restrict__ rows, int range, int ranges, int parts, int32_t* status) {
   extern __shared__ __align__(16) uint32_t smem[];
-  uint32_t* keys = smem;                      // token | prompt << 31
-  uint32_t* times = smem + SLOTS;
-  __shared__ int s_b;
-  __shared__ int64_t s_slice;
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i < SLOTS / 4; i += BUILD_THREADS) {
-    ((uint4*)keys)[i] = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
-    ((uint4*)times)[i] = make_uint4(0, 0, 0, 0);
-  }
+  uint32_t* cnt = smem;                       // [range / 2]: two counts a word
+  uint32_t* seen = smem + range / 2;          // [range / 32]: tokens of the prompt
+  const int tid = threadIdx.x;
+  const int part = (int)(blockIdx.x % parts), which = (int)(blockIdx.x / parts % ranges), b = (int)(blockIdx.x / parts / ranges);
+  for (int i = tid; i < build_smem(range) / 16; i += BUILD_THREADS) ((uint4*)smem)[i] = make_uint4(0, 0, 0, 0);
   griddep_wait();                // the previous kernel's writes are visible from here on
   griddep_launch_dependents();
-  // this CTA's slice: the blockIdx.x-th of all the requests' slices
-  if (tid < 32) {
-    int64_t before = 0;
-    int found = -1;
-    for (int b0 = 0; b0 < B && found < 0; b0 += 32) {
-      const int b = b0 + lane;
-      int64_t n = 0;
-      if (b < B) n = ceil_div(max((int64_t)0, min((int64_t)offsets[b + 1], S) - (int64_t)offsets[b]), SLICE);
-      int64_t upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const unsigned who = __ballot_sync(0xffffffffu, before + upto > (int64_t)blockIdx.x);
-      if (who) {
-        found = b0 + __ffs(who) - 1;
-        before += __shfl_sync(0xffffffffu, upto - n, __ffs(who) - 1);
-      } else {
-        before += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (lane == 0) {
-      s_b = found;
-      s_slice = (int64_t)blockIdx.x - before;
-    }
-    // the requests that end past the tokens, once
-    if (blockIdx.x == 0)
-      for (int b = lane; b < B; b += 32)
-        if ((int64_t)offsets[b + 1] > S) flag_status(status, MTPSD_STATUS_ROW_RANGE);
-  }
+  const bool first_cta = which == 0 && part == 0;
+  const int64_t row = own_table_row(rows, b, n_rows, first_cta ? status : nullptr);
+  const int64_t first = offsets[b], stop = offsets[b + 1], end = min(stop, S);
+  if (first_cta && tid == 0 && stop > S) flag_status(status, MTPSD_STATUS_ROW_RANGE);
+  if (row < 0) return;           // the whole cluster
+  const int64_t n = max(end - first, (int64_t)0), cut = n_prompt ? first + n_prompt[b] : end;
+  const int64_t j0 = first + n * part / parts, j1 = first + n * (part + 1) / parts;
+  const int64_t base = (int64_t)which * range;
   __syncthreads();
-  const int b = s_b;
-  if (b < 0) return;             // the launch has a CTA per request to spare
-  const int64_t row = own_table_row(rows, b, n_rows, nullptr);      // flagged when the rows were cleared
-  if (row < 0) return;
-  const int64_t first = offsets[b], end = min((int64_t)offsets[b + 1], S);
-  const int64_t j0 = first + s_slice * SLICE, j1 = min(j0 + SLICE, end);
-  const int64_t cut = n_prompt ? first + n_prompt[b] : end;
-  constexpr int U = SLICE / BUILD_THREADS;
-  int64_t t[U];
+  constexpr int U = 8;
+  for (int64_t block = j0; block < j1; block += BLOCK) {
+    const int64_t stop_at = min(block + BLOCK, j1);
+    for (int64_t j = block + tid; j < stop_at; j += U * BUILD_THREADS) {
+      int64_t t[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) t[u] = j0 + tid + u * BUILD_THREADS < j1 ? tokens[j0 + tid + u * BUILD_THREADS] : -1;
+      for (int u = 0; u < U; ++u) t[u] = j + u * BUILD_THREADS < stop_at ? __ldg(tokens + j + u * BUILD_THREADS) : -1;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t j = j0 + tid + u * BUILD_THREADS;
-    if (j >= j1) break;
-    if (t[u] < 0 || t[u] >= V) {
-      flag_status(status, MTPSD_STATUS_INDEX_RANGE);
-      continue;
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = j + u * BUILD_THREADS, c = t[u] - base;
+        if (at >= stop_at) break;
+        if (which == 0 && (t[u] < 0 || t[u] >= V)) flag_status(status, MTPSD_STATUS_INDEX_RANGE);
+        if (c < 0 || c >= range || t[u] >= V) continue;
+        if (at < cut) {
+          // looked at first: a frequent token's bit is set already
+          const uint32_t bit = 1u << (c & 31);
+          if (!(((volatile uint32_t*)seen)[c >> 5] & bit)) atomicOr(&seen[c >> 5], bit);
+        } else {
+          atomicAdd(&cnt[c >> 1], (c & 1) ? 65536u : 1u);
+        }
+      }
     }
-    const bool prompt = j < cut;
-    const uint32_t key = (uint32_t)t[u] | (prompt ? 0x80000000u : 0u);
-    uint32_t slot = key * 2654435761u >> 19;  // 13 bits
-    for (;;) {                   // at most half the slots are taken: an empty one or the key's is found
-      uint32_t k = ((volatile uint32_t*)keys)[slot];
-      if (k == EMPTY) k = atomicCAS(&keys[slot], EMPTY, key);
-      if (k == EMPTY || k == key) break;
-      slot = (slot + 1) & (SLOTS - 1);
+    if (stop_at < j1) {
+      __syncthreads();
+      for (int i = tid; i < range / 2; i += BUILD_THREADS) cnt[i] = limit2(cnt[i]);
+      __syncthreads();
     }
-    if (!prompt) atomicAdd(&times[slot], 1u);
   }
-  __syncthreads();
-  int16_t* at = counts + row * ld;
-  const bool below = end - first <= 0x7fff;   // no count of this request can pass the limit
-  for (int i = tid; i < SLOTS; i += BUILD_THREADS) {
-    const uint32_t key = keys[i];
-    if (key == EMPTY) continue;
-    const int64_t tok = key & 0x7fffffffu;
-    uint32_t* w = (uint32_t*)(at + (tok & ~(int64_t)1));
-    const int sh = (tok & 1) ? 16 : 0;
-    if (key >> 31) atomicOr(w, 0x8000u << sh);
-    else if (below) atomicAdd(w, times[i] << sh);
-    else add_word(at, tok, times[i]);
+  // the words of this CTA's share of the range: eight a thread and step
+  if (parts > 1) cluster_sync();
+  else __syncthreads();
+  const int64_t width = min((int64_t)range, ld - base);            // <= 0: a range past the row
+  const int g0 = (int)(max(width, (int64_t)0) / 8 * part / parts), g1 = (int)(max(width, (int64_t)0) / 8 * (part + 1) / parts);
+  for (int g = g0 + tid; g < g1; g += BUILD_THREADS) {
+    uint32_t sum[4] = {0, 0, 0, 0}, bits = 0;
+    if (parts == 1) {
+      const uint4 v = ((const uint4*)cnt)[g];
+      sum[0] = limit2(v.x); sum[1] = limit2(v.y); sum[2] = limit2(v.z); sum[3] = limit2(v.w);
+      bits = ((const uint8_t*)seen)[g];
+    } else {
+      for (int r = 0; r < parts; ++r) {
+        const uint4 v = ld_peer((const uint4*)cnt + g, r);
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+        bits |= ld_peer_u8((const uint8_t*)seen + g, r);
+        // each half at most 32767 before and after, so that a sum stays within 16 bits
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = limit2(sum[e] + limit2(k[e]));
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = sum[e] | (bits >> (2 * e) & 1u) << 15 | (bits >> (2 * e + 1) & 1u) << 31;
+    *(uint4*)(counts + row * ld + base + 8 * (int64_t)g) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // a row wider than the vocabulary: zeros
+  if (which == ranges - 1)
+    for (int64_t c = (int64_t)ranges * range + 8 * (part * BUILD_THREADS + tid); c < ld; c += 8 * (int64_t)parts * BUILD_THREADS)
+      *(uint4*)(counts + row * ld + c) = make_uint4(0, 0, 0, 0);
+  if (parts > 1) cluster_sync();              // no CTA leaves while another reads its counts
 }
-static_assert(SLOTS == 1 << 13, "the hash gives a slot");
 
 __global__ void __launch_bounds__(256) token_counts_accept_kernel(const int64_t* __restrict__ draft,
                                                                   const int32_t* __restrict__ n_acc,
@@ -193,17 +189,36 @@ int launch_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* 
                               int64_t V, int16_t* counts, int64_t ld, int n_rows, const int32_t* rows, int32_t* status,
                               cudaStream_t st) {
   static std::atomic<uint64_t> attr;
-  if (!set_smem_limit_once(token_counts_build_kernel, BUILD_SMEM, attr)) {
+  if (!set_smem_limit_once(token_counts_build_kernel, build_smem(MAX_RANGE), attr)) {
     set_error("token_counts_build: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
   }
-  const int per_row = (int)ceil_div(ld / 8, CLEAR_THREADS * CLEAR_VECS);
-  launch_k(token_counts_clear_kernel, dim3(per_row, B), CLEAR_THREADS, 0, st, counts, ld, n_rows, rows, status);
-  if (int rc = check_launch("token_counts_build")) return rc;
-  // a slice per 4096 tokens and one for what is left of each request
-  const int64_t slices = S / SLICE + B;
-  launch_k(token_counts_build_kernel, (unsigned)slices, BUILD_THREADS, BUILD_SMEM, st, tokens, S, offsets, n_prompt, B, V,
-           counts, ld, n_rows, rows, status);
+  const int ranges = (int)ceil_div(V, MAX_RANGE);
+  const int range = (int)(ceil_div(ceil_div(V, ranges), 128) * 128);
+  // parts of a request's tokens: while there are fewer CTAs than four for every SM, and more than 4096 tokens for a part
+  int parts = 1;
+  while (parts < MAX_PARTS && (int64_t)B * ranges * parts * 2 <= 4 * num_sms() && S / (2 * parts) >= 4096) parts *= 2;
+  const int64_t grid = (int64_t)B * ranges * parts;
+  if (grid > 0x7fffffffLL) {
+    set_error("token_counts_build: too many requests for this vocabulary");
+    return MTPSD_EUNSUPPORTED;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(BUILD_THREADS);
+  cfg.dynamicSmemBytes = build_smem(range);
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = parts;
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, token_counts_build_kernel, tokens, S, offsets, n_prompt, V, counts, ld, n_rows, rows, range, ranges,
+                     parts, status);
   return check_launch("token_counts_build");
 }
 
