@@ -489,60 +489,87 @@ def kv_writeback_slots(src_latent, src_idxk, src_idxs, num_accepted, dst_latent,
 
 # --------------------------------------------------------------------------- head and logits
 
-def _need_rows(t, name: str, dtypes, shape):
-    """A 2-D CUDA tensor of the given shape whose rows are contiguous (any row stride >= the row)."""
+def _current(t, name: str) -> int:
+    """The current device, on whose stream the launch goes: every tensor has to be there, t the first of them."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _tensor(t, name: str, dev: int, dtype, ndim: int):
+    """Checks a contiguous tensor on device dev; returns its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dev: int, dtypes, R: int, V: int):
+    """Checks a tensor [R, V] on device dev whose rows are contiguous; returns its address and its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}, is on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dim() != 2 or t.shape[0] != R or t.shape[1] != V:
+        raise ValueError(f"{name} must be [{R}, {V}], got {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), max(V, 1)
+    ld, step = t.stride()
+    if R and V > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if R > 1 and ld < V:
         raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), ld if R > 1 else max(V, 1)
 
 
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _status_ptr(t, dev: int):
+    if t is None:
+        return None
+    if t.numel() < 1:
+        raise ValueError("dev_status must hold one int32")
+    return _tensor(t, "dev_status", dev, torch.int32, t.dim())
 
 
-def _here(*tensors):
-    """Every tensor on the current device: the launch goes to the current device's stream."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _need_status(t):
-    if t is not None:
-        _need(t, "dev_status", torch.int32)
-        if t.numel() < 1:
-            raise ValueError("dev_status must hold one int32")
+_OUT_TYPES = (torch.bfloat16, torch.float32)
+_F32_ONLY = (torch.float32,)
 
 
 def gemm_fp8_block128(a, a_scale, w, w_scale, out=None, out_dtype=None, dev_status=None, stream=None):
     """out [M, N] = the product of E4M3 codes a [M, K] and w [N, K] (uint8) with a float32 scale per block of 128:
     a_scale [M, K/128]; w_scale [N, K/128] (quantize_fp8_block128 of the weight) or [ceil(N/128), K/128] (128 x 128
     blocks).  out is bf16 (or out_dtype float32); an out given may have any row stride."""
-    _need(a, "a", torch.uint8, 2)
-    _need(w, "w", torch.uint8, 2)
+    dev = _current(a, "a")
+    pa, pw = _tensor(a, "a", dev, torch.uint8, 2), _tensor(w, "w", dev, torch.uint8, 2)
     M, K = a.shape
-    n_out = w.shape[0]
-    if w.shape[1] != K:
+    n_out, k_w = w.shape
+    if k_w != K:
         raise ValueError("a and w must have the same K")
     if K % 128:
         raise ValueError("K must be a multiple of 128")
-    _need(a_scale, "a_scale", torch.float32)
-    _need(w_scale, "w_scale", torch.float32, 2)
-    if a_scale.shape not in ((M, K // 128), (M * (K // 128),)):
+    kbs = K // 128
+    psa, psw = _tensor(a_scale, "a_scale", dev, torch.float32, a_scale.dim()), _tensor(w_scale, "w_scale", dev, torch.float32, 2)
+    if a_scale.shape not in ((M, kbs), (M * kbs,)):
         raise ValueError("a_scale must be [M, K/128]")
-    if w_scale.shape == (n_out, K // 128):
+    if w_scale.shape == (n_out, kbs):
         rows = 1
-    elif w_scale.shape == (-(-n_out // 128), K // 128):
+    elif w_scale.shape == (-(-n_out // 128), kbs):
         rows = 128
     else:
         raise ValueError("w_scale must be [N, K/128] or [ceil(N/128), K/128]")
@@ -550,13 +577,10 @@ def gemm_fp8_block128(a, a_scale, w, w_scale, out=None, out_dtype=None, dev_stat
         out = torch.empty(M, n_out, dtype=out_dtype or torch.bfloat16, device=a.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    _need_rows(out, "out", (torch.bfloat16, torch.float32), (M, n_out))
-    _need_status(dev_status)
-    _here(a, a_scale, w, w_scale, out, dev_status)
+    po, ld = _rows(out, "out", dev, _OUT_TYPES, M, n_out)
     check("mtpsd_gemm_fp8_block128", lib().mtpsd_gemm_fp8_block128(
-        _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), rows, M, n_out, K,
-        N.MTPSD_F32 if out.dtype == torch.float32 else N.MTPSD_BF16, _ptr(out), _row_stride(out), _ptr(dev_status),
-        _stream(stream)))
+        pa, psa, pw, psw, rows, M, n_out, K, N.MTPSD_F32 if out.dtype == torch.float32 else N.MTPSD_BF16, po, ld,
+        _status_ptr(dev_status, dev), _raw_stream(stream, dev)))
     return out
 
 
@@ -565,16 +589,19 @@ def token_counts_ld(V: int) -> int:
     return int(lib().mtpsd_token_counts_ld(V))
 
 
-def _need_counts(counts, V, B, count_rows):
-    _need(counts, "counts", torch.int16, 2)
-    if counts.shape[1] < V or counts.shape[1] % 8:
+def _counts(counts, V, B, count_rows, dev):
+    """Checks a token table and the requests' rows in it; returns their addresses."""
+    p = _tensor(counts, "counts", dev, torch.int16, 2)
+    n_rows, ld = counts.shape
+    if ld < V or ld % 8:
         raise ValueError("counts rows must have at least V words, a multiple of 8 (token_counts_ld)")
-    if count_rows is not None:
-        _need(count_rows, "count_rows", torch.int32, 1)
-        if count_rows.numel() != B:
-            raise ValueError("count_rows must have one entry per request")
-    elif counts.shape[0] < B:
-        raise ValueError("counts has fewer rows than requests")
+    if count_rows is None:
+        if n_rows < B:
+            raise ValueError("counts has fewer rows than requests")
+        return p, None
+    if count_rows.numel() != B:
+        raise ValueError("count_rows must have one entry per request")
+    return p, _tensor(count_rows, "count_rows", dev, torch.int32, 1)
 
 
 def token_counts_build(tokens, offsets, V: int, n_prompt=None, counts=None, count_rows=None, dev_status=None,
@@ -582,48 +609,45 @@ def token_counts_build(tokens, offsets, V: int, n_prompt=None, counts=None, coun
     """The token table rows of B requests from their tokens [S] int64 (ragged, offsets [B+1] uint32): the first
     n_prompt[b] (int64; all without it) set the prompt bit, the others count as output.  Request b fills row b, or
     count_rows[b] of a larger table."""
-    _need(tokens, "tokens", torch.int64, 1)
-    _need(offsets, "offsets", torch.uint32, 1)
+    dev = _current(tokens, "tokens")
+    pt, po = _tensor(tokens, "tokens", dev, torch.int64, 1), _tensor(offsets, "offsets", dev, torch.uint32, 1)
     B = offsets.numel() - 1
     if B < 0:
         raise ValueError("offsets must have B+1 entries")
+    pn = None
     if n_prompt is not None:
-        _need(n_prompt, "n_prompt", torch.int64, 1)
+        pn = _tensor(n_prompt, "n_prompt", dev, torch.int64, 1)
         if n_prompt.numel() != B:
             raise ValueError("n_prompt must have one entry per request")
     if counts is None:
         if count_rows is not None:
             raise ValueError("count_rows needs a table")
         counts = torch.empty(B, token_counts_ld(V), dtype=torch.int16, device=tokens.device)
-    _need_counts(counts, V, B, count_rows)
-    _need_status(dev_status)
-    _here(tokens, offsets, n_prompt, counts, count_rows, dev_status)
+    pc, pr = _counts(counts, V, B, count_rows, dev)
     check("mtpsd_token_counts_build", lib().mtpsd_token_counts_build(
-        _ptr(tokens), tokens.numel(), _ptr(offsets), _ptr(n_prompt), B, V, _ptr(counts), counts.shape[1],
-        counts.shape[0], _ptr(count_rows), _ptr(dev_status), _stream(stream)))
+        pt, tokens.numel(), po, pn, B, V, pc, counts.shape[1], counts.shape[0], pr, _status_ptr(dev_status, dev),
+        _raw_stream(stream, dev)))
     return counts
 
 
 def token_counts_accept(counts, V: int, draft, num_accepted, next_tokens, count_rows=None, dev_status=None, stream=None):
     """Adds draft[b, :num_accepted[b]] and next_tokens[b] to the token table (in place); draft and num_accepted may be
     None (one token per request)."""
-    _need(next_tokens, "next_tokens", torch.int64, 1)
+    dev = _current(next_tokens, "next_tokens")
+    px = _tensor(next_tokens, "next_tokens", dev, torch.int64, 1)
     B = next_tokens.numel()
-    K = 0
+    K, pd, pn = 0, None, None
     if (draft is None) != (num_accepted is None):
         raise ValueError("give draft and num_accepted together or neither")
     if draft is not None:
-        _need(draft, "draft", torch.int64, 2)
-        _need(num_accepted, "num_accepted", torch.int32, 1)
+        pd, pn = _tensor(draft, "draft", dev, torch.int64, 2), _tensor(num_accepted, "num_accepted", dev, torch.int32, 1)
         K = draft.shape[1]
         if draft.shape[0] != B or num_accepted.numel() != B:
             raise ValueError("draft [B, K], num_accepted [B] and next_tokens [B] must have the same B")
-    _need_counts(counts, V, B, count_rows)
-    _need_status(dev_status)
-    _here(counts, draft, num_accepted, next_tokens, count_rows, dev_status)
+    pc, pr = _counts(counts, V, B, count_rows, dev)
     check("mtpsd_token_counts_accept", lib().mtpsd_token_counts_accept(
-        _ptr(draft), _ptr(num_accepted), _ptr(next_tokens), B, K, V, _ptr(counts), counts.shape[1], counts.shape[0],
-        _ptr(count_rows), _ptr(dev_status), _stream(stream)))
+        pd, pn, px, B, K, V, pc, counts.shape[1], counts.shape[0], pr, _status_ptr(dev_status, dev),
+        _raw_stream(stream, dev)))
     return counts
 
 
@@ -638,73 +662,71 @@ def process_logits(logits, row_offsets, draft=None, counts=None, count_rows=None
     request, or count_rows [B] int32); repetition, frequency, presence, temperature [B] float32; biases as ragged lists
     (bias_offsets [B+1] uint32, bias_tokens int32, bias_values float32); bitmask [n, ceil(V/32)] int32, one row per
     logits row, or mask_rows [R] int32 (-1: none)."""
-    if not isinstance(logits, torch.Tensor):
-        raise TypeError("logits must be a torch tensor")
+    dev = _current(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [R, V]")
     R, V = logits.shape
-    _need_rows(logits, "logits", (torch.bfloat16, torch.float32), (R, V))
-    _need(row_offsets, "row_offsets", torch.uint32, 1)
+    px, ld = _rows(logits, "logits", dev, _OUT_TYPES, R, V)
+    po = _tensor(row_offsets, "row_offsets", dev, torch.uint32, 1)
     B = row_offsets.numel() - 1
-    K = 0
+    K, pd = 0, None
     if draft is not None:
-        _need(draft, "draft", torch.int64, 2)
+        pd = _tensor(draft, "draft", dev, torch.int64, 2)
         if draft.shape[0] != B:
             raise ValueError("draft must be [B, K]")
         K = draft.shape[1]
+    pc = pr = None
+    c_ld = c_rows = 0
     if counts is not None:
-        _need_counts(counts, V, B, count_rows)
+        pc, pr = _counts(counts, V, B, count_rows, dev)
+        c_rows, c_ld = counts.shape
     elif count_rows is not None:
         raise ValueError("count_rows without counts")
-    for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence),
-                    ("temperature", temperature)):
-        if t is not None:
-            _need(t, name, torch.float32, 1)
-            if t.numel() != B:
-                raise ValueError(f"{name} must have one entry per request")
-    given = [t is not None for t in (bias_offsets, bias_tokens, bias_values)]
-    if any(given) and not all(given):
-        raise ValueError("give bias_offsets, bias_tokens and bias_values together or none")
-    if bias_offsets is not None:
-        _need(bias_offsets, "bias_offsets", torch.uint32, 1)
-        _need(bias_tokens, "bias_tokens", torch.int32, 1)
-        _need(bias_values, "bias_values", torch.float32, 1)
-        if bias_offsets.numel() != B + 1 or bias_tokens.numel() != bias_values.numel():
+
+    def per_request(t, name):
+        if t is None:
+            return None
+        p = _tensor(t, name, dev, torch.float32, 1)
+        if t.numel() != B:
+            raise ValueError(f"{name} must have one entry per request")
+        return p
+
+    p_rep, p_freq = per_request(repetition, "repetition"), per_request(frequency, "frequency")
+    p_pres, p_temp = per_request(presence, "presence"), per_request(temperature, "temperature")
+    p_bo = p_bt = p_bv = None
+    n_bias = 0
+    if bias_offsets is not None or bias_tokens is not None or bias_values is not None:
+        if bias_offsets is None or bias_tokens is None or bias_values is None:
+            raise ValueError("give bias_offsets, bias_tokens and bias_values together or none")
+        p_bo = _tensor(bias_offsets, "bias_offsets", dev, torch.uint32, 1)
+        p_bt = _tensor(bias_tokens, "bias_tokens", dev, torch.int32, 1)
+        p_bv = _tensor(bias_values, "bias_values", dev, torch.float32, 1)
+        n_bias = bias_tokens.numel()
+        if bias_offsets.numel() != B + 1 or bias_values.numel() != n_bias:
             raise ValueError("bias_offsets must be [B+1], bias_tokens and bias_values of one length")
+    p_mask = p_mrows = None
+    n_masks = 0
     if bitmask is not None:
-        _need(bitmask, "bitmask", torch.int32, 2)
-        if bitmask.shape[1] != -(-V // 32):
+        p_mask = _tensor(bitmask, "bitmask", dev, torch.int32, 2)
+        n_masks, words = bitmask.shape
+        if words != -(-V // 32):
             raise ValueError("bitmask rows must have ceil(V/32) words")
     if mask_rows is not None:
-        _need(mask_rows, "mask_rows", torch.int32, 1)
+        p_mrows = _tensor(mask_rows, "mask_rows", dev, torch.int32, 1)
         if mask_rows.numel() != R:
             raise ValueError("mask_rows must have one entry per row")
     if argmax is None and probs is None and out_logits is None:
         argmax = torch.empty(R, dtype=torch.int64, device=logits.device)
+    p_arg = None
     if argmax is not None:
-        _need(argmax, "argmax", torch.int64)
         if argmax.numel() != R:
             raise ValueError("argmax must have one entry per row")
-    for name, t in (("probs", probs), ("out_logits", out_logits)):
-        if t is not None:
-            _need_rows(t, name, (torch.float32,), (R, V))
-    _need_status(dev_status)
-    _here(logits, row_offsets, draft, counts, count_rows, repetition, frequency, presence, bias_offsets, bias_tokens,
-          bias_values, bitmask, mask_rows, temperature, argmax, probs, out_logits, dev_status)
-
-    def p(t):
-        return None if t is None else t.data_ptr()
-
-    a = N.LogitsArgs(B=B, R=R, V=V, dtype=N.MTPSD_F32 if logits.dtype == torch.float32 else N.MTPSD_BF16, K=K,
-                     logits=p(logits), ld=_row_stride(logits), row_offsets=p(row_offsets), counts=p(counts),
-                     counts_ld=0 if counts is None else counts.shape[1],
-                     counts_rows=0 if counts is None else counts.shape[0],
-                     n_bias=0 if bias_tokens is None else bias_tokens.numel(), count_rows=p(count_rows), draft=p(draft),
-                     repetition=p(repetition), frequency=p(frequency), presence=p(presence),
-                     bias_offsets=p(bias_offsets), bias_tokens=p(bias_tokens), bias_values=p(bias_values),
-                     bitmask=p(bitmask), mask_rows=p(mask_rows), n_masks=0 if bitmask is None else bitmask.shape[0],
-                     temperature=p(temperature), argmax=p(argmax), probs=p(probs),
-                     probs_ld=0 if probs is None else _row_stride(probs), out_logits=p(out_logits),
-                     out_ld=0 if out_logits is None else _row_stride(out_logits), dev_status=p(dev_status))
-    check("mtpsd_process_logits", lib().mtpsd_process_logits(C.byref(a), _stream(stream)))
+        p_arg = _tensor(argmax, "argmax", dev, torch.int64, argmax.dim())
+    p_probs, ld_probs = (None, 0) if probs is None else _rows(probs, "probs", dev, _F32_ONLY, R, V)
+    p_out, ld_out = (None, 0) if out_logits is None else _rows(out_logits, "out_logits", dev, _F32_ONLY, R, V)
+    # in the order of the structure's fields
+    a = N.LogitsArgs(B, R, V, N.MTPSD_F32 if logits.dtype == torch.float32 else N.MTPSD_BF16, K, px, ld, po, pc, c_ld, c_rows,
+                     n_bias, pr, pd, p_rep, p_freq, p_pres, p_bo, p_bt, p_bv, p_mask, p_mrows, n_masks, p_temp, p_arg,
+                     p_probs, ld_probs, p_out, ld_out, _status_ptr(dev_status, dev))
+    check("mtpsd_process_logits", lib().mtpsd_process_logits(C.byref(a), _raw_stream(stream, dev)))
     return argmax

@@ -427,8 +427,8 @@ int mtpsd_gemm_fp8_block128(const uint8_t* a, const float* a_scale, const uint8_
   if (M == 0 || N == 0) return MTPSD_OK;
   if (!out || (K > 0 && (!a || !a_scale || !w || !w_scale))) return fail(MTPSD_EINVAL, "gemm_fp8_block128: null pointer");
   if (!aligned(a, 16) || !aligned(w, 16)) return fail(MTPSD_EINVAL, "gemm_fp8_block128: a and w must be 16-byte aligned");
-  if (!aligned(out, out_dtype == MTPSD_F32 ? 4 : 2) || !aligned(a_scale, 4) || !aligned(w_scale, 4))
-    return fail(MTPSD_EINVAL, "gemm_fp8_block128: out and the scales must be aligned to their elements");
+  if (!aligned(out, out_dtype == MTPSD_F32 ? 4 : 2) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(dev_status, 4))
+    return fail(MTPSD_EINVAL, "gemm_fp8_block128: out, the scales and dev_status must be aligned to their elements");
   GemmFp8Plan p;
   p.a = a; p.a_scale = a_scale; p.w = w; p.w_scale = w_scale; p.w_scale_rows = w_scale_rows;
   p.M = M; p.N = N; p.K = K; p.out_f32 = out_dtype == MTPSD_F32; p.out = out; p.ld_out = ld_out; p.status = dev_status;
@@ -438,11 +438,13 @@ int mtpsd_gemm_fp8_block128(const uint8_t* a, const float* a_scale, const uint8_
 int64_t mtpsd_token_counts_ld(int64_t V) { return V > 0 ? (V + 7) / 8 * 8 : 0; }
 
 // The checks that the calls on the token table share.
-static int check_counts(const void* counts, int64_t V, int64_t ld, int32_t n_rows, int32_t B, bool has_rows, const char* who) {
+static int check_counts(const void* counts, int64_t V, int64_t ld, int32_t n_rows, int32_t B, const int32_t* rows,
+                        const char* who) {
   if (V < 1 || V > 0x7fffffffLL) return fail(MTPSD_EINVAL, "%s: need 1 <= V < 2^31", who);
   if (!counts || !aligned(counts, 16)) return fail(MTPSD_EINVAL, "%s: counts must be given and 16-byte aligned", who);
   if (ld < V || ld % 8) return fail(MTPSD_EINVAL, "%s: the table's row stride must be a multiple of 8 and at least V", who);
-  if (n_rows < 0 || (!has_rows && n_rows < B)) return fail(MTPSD_EINVAL, "%s: the table has fewer rows than requests", who);
+  if (n_rows < 0 || (!rows && n_rows < B)) return fail(MTPSD_EINVAL, "%s: the table has fewer rows than requests", who);
+  if (!aligned(rows, 4)) return fail(MTPSD_EINVAL, "%s: count_rows must be aligned to its elements", who);
   return MTPSD_OK;
 }
 
@@ -452,8 +454,10 @@ int mtpsd_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* o
   g_err[0] = 0;
   if (B < 0 || S < 0 || S > 0xffffffffLL) return fail(MTPSD_EINVAL, "token_counts_build: need B >= 0, 0 <= S < 2^32");
   if (B == 0) return MTPSD_OK;
-  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows != nullptr, "token_counts_build")) return rc;
+  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows, "token_counts_build")) return rc;
   if (!offsets || (S > 0 && !tokens)) return fail(MTPSD_EINVAL, "token_counts_build: null pointer");
+  if (!aligned(tokens, 8) || !aligned(offsets, 4) || !aligned(n_prompt, 8) || !aligned(dev_status, 4))
+    return fail(MTPSD_EINVAL, "token_counts_build: an array is not aligned to its elements");
   return launch_token_counts_build(tokens, S, offsets, n_prompt, B, V, counts, ld, n_rows, count_rows, dev_status,
                                    (cudaStream_t)stream);
 }
@@ -465,8 +469,10 @@ int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted,
   if (B < 0 || K < 0 || (int64_t)B * ((int64_t)K + 1) > 0x7fffffffLL)
     return fail(MTPSD_EINVAL, "token_counts_accept: need B >= 0, K >= 0, B * (K + 1) < 2^31");
   if (B == 0) return MTPSD_OK;
-  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows != nullptr, "token_counts_accept")) return rc;
+  if (int rc = check_counts(counts, V, ld, n_rows, B, count_rows, "token_counts_accept")) return rc;
   if (!next_tokens || (K > 0 && (!draft || !num_accepted))) return fail(MTPSD_EINVAL, "token_counts_accept: null pointer");
+  if (!aligned(draft, 8) || !aligned(num_accepted, 4) || !aligned(next_tokens, 8) || !aligned(dev_status, 4))
+    return fail(MTPSD_EINVAL, "token_counts_accept: an array is not aligned to its elements");
   return launch_token_counts_accept(draft, num_accepted, next_tokens, B, K, V, counts, ld, n_rows, count_rows, dev_status,
                                     (cudaStream_t)stream);
 }
@@ -484,7 +490,8 @@ int mtpsd_process_logits(const mtpsd_logits_args* a, void* stream) {
     return fail(MTPSD_EINVAL, "process_logits: a row stride is below V");
   if (a->R > 0 && !a->argmax && !a->probs && !a->out_logits) return fail(MTPSD_EINVAL, "process_logits: no output given");
   if (a->counts)
-    if (int rc = check_counts(a->counts, a->V, a->counts_ld, a->counts_rows, a->B, a->count_rows != nullptr, "process_logits")) return rc;
+    if (int rc = check_counts(a->counts, a->V, a->counts_ld, a->counts_rows, a->B, a->count_rows,
+                              "process_logits")) return rc;
   if (a->bias_offsets && (a->n_bias < 0 || (a->n_bias > 0 && (!a->bias_tokens || !a->bias_values))))
     return fail(MTPSD_EINVAL, "process_logits: biases need n_bias >= 0, bias_tokens and bias_values");
   if (a->bitmask && (a->n_masks < 0 || (!a->mask_rows && a->n_masks < a->R)))
@@ -494,6 +501,12 @@ int mtpsd_process_logits(const mtpsd_logits_args* a, void* stream) {
   const size_t es = a->dtype == MTPSD_F32 ? 4 : 2;
   if (!aligned(a->logits, es) || !aligned(a->probs, 4) || !aligned(a->out_logits, 4))
     return fail(MTPSD_EINVAL, "process_logits: logits, probs and out_logits must be aligned to their elements");
+  const void* words[] = {a->row_offsets, a->repetition, a->frequency, a->presence, a->bias_offsets, a->bias_tokens,
+                         a->bias_values, a->bitmask, a->mask_rows, a->temperature, a->dev_status};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return fail(MTPSD_EINVAL, "process_logits: an array is not aligned to its elements");
+  if (!aligned(a->draft, 8) || !aligned(a->argmax, 8))
+    return fail(MTPSD_EINVAL, "process_logits: draft and argmax must be aligned to their elements");
   if ((const void*)a->out_logits == a->logits && (a->dtype != MTPSD_F32 || a->out_ld != a->ld))
     return fail(MTPSD_EINVAL, "process_logits: in place needs float32 logits and out_ld == ld");
   return launch_process_logits(*a, (cudaStream_t)stream);

@@ -170,6 +170,30 @@ def test_process_refusals(native):
     assert L.mtpsd_process_logits(C.byref(a), None) == 0
 
 
+def test_misaligned_arrays_are_refused(native):
+    """Every array of integers and floats has to be aligned to its elements: the kernels load whole elements."""
+    L, E = native.lib(), native.MTPSD_EINVAL
+    st = dict(status=None, stream=None)
+    ok = dict(a=16, sa=16, w=16, sw=16, rows=1, M=4, N=8, K=256, dt=native.MTPSD_BF16, out=16, ld=8, **st)
+    for change in (dict(sw=6), dict(status=2)):
+        assert L.mtpsd_gemm_fp8_block128(*{**ok, **change}.values()) == E, change
+    ok = dict(tokens=8, S=4, offsets=8, n_prompt=8, B=2, V=10, counts=16, ld=16, n_rows=2, rows=None, **st)
+    for change in (dict(tokens=12), dict(offsets=6), dict(n_prompt=12), dict(rows=6), dict(status=2)):
+        assert L.mtpsd_token_counts_build(*{**ok, **change}.values()) == E, change
+    ok = dict(draft=8, n_acc=8, nxt=8, B=2, K=3, V=10, counts=16, ld=16, n_rows=2, rows=None, **st)
+    for change in (dict(draft=12), dict(n_acc=6), dict(nxt=12), dict(rows=6), dict(status=2)):
+        assert L.mtpsd_token_counts_accept(*{**ok, **change}.values()) == E, change
+    ok = dict(B=2, R=4, V=40, K=1, dtype=native.MTPSD_F32, logits=16, ld=40, row_offsets=8, argmax=8, draft=8,
+              counts=16, counts_ld=40, counts_rows=2, bias_tokens=8, bias_values=8, n_bias=1, n_masks=4)
+    for field in ("row_offsets", "repetition", "frequency", "presence", "bias_offsets", "bias_tokens", "bias_values",
+                  "bitmask", "mask_rows", "temperature", "dev_status", "count_rows"):
+        a = native.LogitsArgs(**{**ok, field: 10})
+        assert L.mtpsd_process_logits(C.byref(a), None) == E, field
+    for field in ("draft", "argmax"):
+        a = native.LogitsArgs(**{**ok, field: 12})
+        assert L.mtpsd_process_logits(C.byref(a), None) == E, field
+
+
 def test_binding_refuses_host_tensors():
     import mtp_speculative_decode_gb300 as m
     x = torch.zeros(2, 128, dtype=torch.uint8)
