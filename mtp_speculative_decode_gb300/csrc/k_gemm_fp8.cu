@@ -8,12 +8,12 @@
 // the epilogue warps read, scale and add to float32 accumulators in registers
 // while the next blocks' MMAs run into the other buffers.
 //
-// This kernel is for up to 128 rows of a (k_gemm_fp8_pair.cu takes more): one
+// This kernel is for up to 64 rows of a (k_gemm_fp8_pair.cu takes more): one
 // MMA has M = 128 weight rows (operand A) and N = the rows of a, rounded up to
 // 16 (operand B), so the few rows of a cost only as much as there are of them
 // and the weight streams through once.  A tile is `bn` <= 128 outputs: the weight
-// read bounds these calls (16 x 154880 x 6144 runs at 97 % of the measured copy
-// rate), so bn is chosen such that the tiles load every SM alike; TMEM lanes
+// read bounds these calls (16 x 154880 x 6144 runs at 98 % of the measured copy
+// rate, 144 us; 64 rows at 94 %, 153 us), so bn is chosen such that the tiles load every SM alike; TMEM lanes
 // past bn hold products of stale operands and are not stored.
 //
 // The epilogue reads TMEM (lane = output, column = row of a) in the 16x256b
@@ -25,7 +25,9 @@
 //
 // Roles (608 threads, one CTA per SM):
 //   warps 0-15  epilogue: warp w takes the TMEM lanes 32 (w % 4) .. +31 and the columns of quarter w / 4
-//               (four warps per scheduler hide the latency of the TMEM reads).
+//               (four warps per scheduler hide the latency of the TMEM reads).  A block's scales and the probe
+//               of its barrier are fetched before the block in front is added: read after the wait, they made
+//               the chain of a block long enough to show (163 us at 64 x 154880 x 6144).
 //   warp 16     TMA producer: a ring of stages of one block (128 x 128 bytes of w, cols x 128 of a).
 //   warp 17     TMEM allocation and MMA issue.
 //   warp 18     scales: a ring of slots of four blocks' scales of the rows of a and of the weight rows.
@@ -48,26 +50,22 @@ constexpr int MAX_SPLIT = 8;
 constexpr int W_BYTES = TILE_N * KB;
 constexpr int PAD_N = TILE_N + 4;         // row stride (floats) of a partial tile: a fragment's four columns miss each other's banks
 constexpr int TR_LD = 36;                 // the same for the transposed store of 8 columns x 32 outputs
-constexpr int TR_FLOATS = 8 * TR_LD;
+constexpr int TR_FLOATS = 8 * TR_LD;     // per epilogue warp
 
-// NC: a tile has at most 64 NC columns, an epilogue thread 16 NC accumulators
-template <int NC>
-struct Shape {
-  static constexpr int COLS = 64 * NC;
-  static constexpr int STAGE = W_BYTES + COLS * KB;
-  static constexpr int NSTAGE = 192 * 1024 / STAGE;                     // 8, 6
-  static constexpr int NBUF = TMEM_COLS / COLS;                         // TMEM buffers: 8, 4
-  static constexpr int SLOT_FLOATS = SG * (COLS + TILE_N);
-  static constexpr int OFF_SCALE = NSTAGE * STAGE;
-  static constexpr int OFF_TR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;    // per epilogue warp: TR_FLOATS
-  static constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
-  static constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
-  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-  static constexpr int BYTES = OFF_MISC + 16 + 1024;                    // + alignment slack
-  static_assert(BYTES <= 232448, "shared memory per CTA");
-  static_assert(COLS * PAD_N * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
-  static_assert(OFF_BAR % 16 == 0, "barriers are aligned");
-};
+constexpr int COLS = 64;                  // most columns (rows of a) of a tile; 16 per epilogue warp
+constexpr int STAGE = W_BYTES + COLS * KB;
+constexpr int NSTAGE = 192 * 1024 / STAGE;
+constexpr int NBUF = TMEM_COLS / COLS;
+constexpr int SLOT_FLOATS = SG * (COLS + TILE_N);
+constexpr int OFF_SCALE = NSTAGE * STAGE;
+constexpr int OFF_TR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;
+constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
+constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
+constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(COLS * PAD_N * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
+static_assert(OFF_BAR % 16 == 0, "barriers are aligned");
 
 struct Params {
   const float* sa;
@@ -89,31 +87,29 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t off, float v)
   else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
 }
 
-template <int NC>
 __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_w,
                                                               const __grid_constant__ CUtensorMap tmap_a,
                                                               const __grid_constant__ Params p) {
-  using S = Shape<NC>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = (uint64_t*)(sm + S::OFF_BAR);
-  uint64_t* empty = full + S::NSTAGE;
-  uint64_t* t_full = empty + S::NSTAGE;
-  uint64_t* t_empty = t_full + S::NBUF;
-  uint64_t* s_full = t_empty + S::NBUF;
+  uint8_t* sm = smem_raw + (-saddr(smem_raw) & 1023u);     // no cast: loads stay loads of shared memory
+  uint64_t* full = (uint64_t*)(sm + OFF_BAR);
+  uint64_t* empty = full + NSTAGE;
+  uint64_t* t_full = empty + NSTAGE;
+  uint64_t* t_empty = t_full + NBUF;
+  uint64_t* s_full = t_empty + NBUF;
   uint64_t* s_empty = s_full + NSLOT;
   uint64_t* drain = s_empty + NSLOT;
-  uint32_t* tmem_slot = (uint32_t*)(sm + S::OFF_MISC);
-  volatile int* abort_flag = (volatile int*)(sm + S::OFF_MISC + 4);
-  float* scales = (float*)(sm + S::OFF_SCALE);
+  uint32_t* tmem_slot = (uint32_t*)(sm + OFF_MISC);
+  volatile int* abort_flag = (volatile int*)(sm + OFF_MISC + 4);
+  float* scales = (float*)(sm + OFF_SCALE);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::NSTAGE; ++i) {
+    for (int i = 0; i < NSTAGE; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < S::NBUF; ++i) {
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(&t_full[i], 1);
       mbar_init(&t_empty[i], EPI_WARPS);
     }
@@ -146,7 +142,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   const int first = (int)blockIdx.x / p.split, step = (int)gridDim.x / p.split;   // this cluster's tiles
   const int kb0 = (int)((int64_t)rank * p.kbs / p.split), kb1 = (int)((int64_t)(rank + 1) * p.kbs / p.split);
   // acc[4 j + 2 h + i]: columns 8 j + 2 (lane % 4), +1 of the warp's, output 16 h + 8 i + lane / 4 of its 32
-  uint64_t acc[8 * NC];
+  uint64_t acc[8];
 
   if (warp == PRODUCER_WARP) {
     int n = 0;
@@ -155,11 +151,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const int n0 = tile * p.bn;
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int stage = n % S::NSTAGE, round = n / S::NSTAGE;
+        const int stage = n % NSTAGE, round = n / NSTAGE;
         if (round > 0) ok = wait_all(&empty[stage], (round - 1) & 1, abort_flag, p.status);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t dst = saddr(sm + stage * S::STAGE);
+          const uint32_t dst = saddr(sm + stage * STAGE);
           mbar_expect_tx(&full[stage], bytes);
           tma_load_2d(dst, &tmap_w, kb * KB, n0, &full[stage]);
           tma_load_2d(dst + W_BYTES, &tmap_a, kb * KB, 0, &full[stage]);
@@ -169,8 +165,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     }
     if (*abort_flag && lane == 0) {   // drain this CTA's copies still in flight (bounded)
       volatile int dummy = 0;
-      for (int s = 0; s < S::NSTAGE; ++s) {
-        const int issued = n / S::NSTAGE + (s < n % S::NSTAGE ? 1 : 0);   // loads of stage s
+      for (int s = 0; s < NSTAGE; ++s) {
+        const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);   // loads of stage s
         if (issued > 0) mbar::wait<false>(&full[s], (issued - 1) & 1, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
       }
     }
@@ -180,14 +176,14 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     const uint32_t id = idesc_n(p.cols);
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int stage = n % S::NSTAGE, buf = n % S::NBUF, round = n / S::NBUF;
-        ok = wait_all(&full[stage], (n / S::NSTAGE) & 1, abort_flag, p.status);
+        const int stage = n % NSTAGE, buf = n % NBUF, round = n / NBUF;
+        ok = wait_all(&full[stage], (n / NSTAGE) & 1, abort_flag, p.status);
         if (ok && round > 0) ok = wait_all(&t_empty[buf], (round - 1) & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t w_base = saddr(sm + stage * S::STAGE), a_base = w_base + W_BYTES;
-          const uint32_t d = tmem_base + (uint32_t)(buf * S::COLS);
+          const uint32_t w_base = saddr(sm + stage * STAGE), a_base = w_base + W_BYTES;
+          const uint32_t d = tmem_base + (uint32_t)(buf * COLS);
 #pragma unroll
           for (int kk = 0; kk < KB / 32; ++kk)
             mma_fp8(d, sw128_desc(w_base + kk * 32), sw128_desc(a_base + kk * 32), id, kk > 0 ? 1u : 0u);
@@ -221,10 +217,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     };
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       for (int kb = kb0; kb < kb1; kb += SG, ++n) {
-        float v[2 * NC][SG], w[4][SG];
+        float v[2][SG], w[4][SG];
         // all of the slot's loads in flight before the wait for its release
 #pragma unroll
-        for (int i = 0; i < 2 * NC; ++i)
+        for (int i = 0; i < 2; ++i)
           if (32 * i < p.cols) load4(p.sa, 32 * i + lane, p.M, kb, v[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -234,89 +230,104 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
         const int slot = n % NSLOT, round = n / NSLOT;
         if (round > 0) ok = wait_all(&s_empty[slot], (round - 1) & 1, abort_flag, p.status);
         if (!ok) break;
-        float* dst = scales + slot * S::SLOT_FLOATS;
+        float* dst = scales + slot * SLOT_FLOATS;
 #pragma unroll
-        for (int i = 0; i < 2 * NC; ++i)
+        for (int i = 0; i < 2; ++i)
           if (32 * i < p.cols)
 #pragma unroll
-            for (int j = 0; j < SG; ++j) dst[j * S::COLS + 32 * i + lane] = v[i][j];
+            for (int j = 0; j < SG; ++j) dst[j * COLS + 32 * i + lane] = v[i][j];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < SG; ++j) dst[SG * S::COLS + j * TILE_N + 32 * i + lane] = w[i][j];
+          for (int j = 0; j < SG; ++j) dst[SG * COLS + j * TILE_N + 32 * i + lane] = w[i][j];
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_full[slot]);
       }
     }
   } else {
-    const int quarter = warp & 3, c0 = (warp >> 2) * 16 * NC;      // this warp's TMEM lanes and first column
+    const int quarter = warp & 3, c0 = (warp >> 2) * 16;           // this warp's TMEM lanes and first column
     const int fr = lane >> 2, fc = 2 * (lane & 3);                 // fragment row and column of this lane
-    const int mine = min(16 * NC, p.cols - c0);                    // columns of the tile (a multiple of 16; <= 0: none)
-    int n = 0, ns = 0;
-    bool ok = true;
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
+    const bool mine = c0 < p.cols;                                 // the warp has columns
+    int n = 0, slot = 0, s_phase = 0;                              // blocks so far, scale slot
+    // A wait that gave up makes the warp walk on without waiting, to the end, and store nothing: the blocks' loop then
+    // has no exit to test for.
+    bool gave_up = false;
+    auto finish = [&](uint64_t* bar, uint32_t parity) {            // of a wait whose first probe failed
+      if (!gave_up) gave_up = !mbar::wait<false>(bar, parity, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+    };
+    for (int tile = first; tile < p.tiles; tile += step) {
 #pragma unroll
-      for (int i = 0; i < 8 * NC; ++i) acc[i] = 0ull;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int slot = ns % NSLOT, j = (kb - kb0) % SG;
-        if (j == 0) ok = wait_all(&s_full[slot], (ns / NSLOT) & 1, abort_flag, p.status);
-        const int buf = n % S::NBUF;
-        if (ok) ok = wait_all(&t_full[buf], (n / S::NBUF) & 1, abort_flag, p.status);
-        if (!ok) break;
+      for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+      // The scales of a block and the probe for its products are fetched while the block before is still being added
+      float wr[4];                                                 // of the thread's four outputs
+      uint64_t cs[2];                                              // of its columns
+      bool ready;
+      auto fetch = [&](int j, int block) {
+        const float* sc = scales + slot * SLOT_FLOATS + j * COLS + c0 + fc;
+        const float* sr = scales + slot * SLOT_FLOATS + SG * COLS + j * TILE_N + quarter * 32 + fr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wr[i] = sr[8 * i];
+        cs[0] = *(const uint64_t*)sc;
+        cs[1] = *(const uint64_t*)(sc + 8);
+        ready = mbar::try_wait<false>(&t_full[block % NBUF], block / NBUF & 1);
+      };
+      auto next_slot = [&]() {
+        if (!mbar::try_wait<false>(&s_full[slot], s_phase)) finish(&s_full[slot], s_phase);
+        __syncwarp();
+      };
+      next_slot();
+      fetch(0, n);
+      for (int kb = kb0, j = 0; kb < kb1; ++kb, ++n) {
+        const int buf = n % NBUF;
+        uint64_t rw[4];
+        const uint64_t s[2] = {cs[0], cs[1]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rw[i] = pack2(make_float2(wr[i], wr[i]));
+        if (!ready) finish(&t_full[buf], n / NBUF & 1);
+        __syncwarp();
         tc_fence_after();
-        const float* sc = scales + slot * S::SLOT_FLOATS + j * S::COLS + c0 + fc;
-        uint64_t rw[4];                                            // the weight scales of the thread's four outputs, twice each
-        const float* sr = scales + slot * S::SLOT_FLOATS + SG * S::COLS + j * TILE_N + quarter * 32 + fr;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rw[i] = pack2(make_float2(sr[8 * i], sr[8 * i]));
-        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * S::COLS + c0);
-#pragma unroll
-        for (int c = 0; c < 16 * NC; c += 32) {                    // 32 columns at a time, 16 at an odd end
-          const int w = 16 * NC - c < 32 ? 16 : 32;
-          if (c >= mine) break;
-          uint32_t t[2][16];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (w == 32) tmem_ld_x4(taddr + ((uint32_t)(16 * h) << 16) + c, t[h]);
-            else tmem_ld_x2(taddr + ((uint32_t)(16 * h) << 16) + c, t[h]);
-          }
+        uint32_t t[2][8];
+        if (mine) {
+          const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * COLS + c0);
+          tmem_ld_x2(taddr, t[0]);
+          tmem_ld_x2(taddr + (16u << 16), t[1]);
           tmem_ld_wait();
-          if (c + 32 >= mine) {                                    // the warp's last read of the buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&t_empty[buf]);
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_empty[buf]);
+        if (++j == SG || kb == kb1 - 1) {                          // every lane has read the slot's scales
+          if (lane == 0) mbar_arrive(&s_empty[slot]);
+          j = 0;
+          if (++slot == NSLOT) {
+            slot = 0;
+            s_phase ^= 1;
           }
+          if (kb < kb1 - 1) next_slot();
+        }
+        if (kb < kb1 - 1) fetch(j, n + 1);
+        if (mine) {
 #pragma unroll
-          for (int g = 0; g < w / 8; ++g) {
-            const uint64_t s = *(const uint64_t*)(sc + c + 8 * g);
+          for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint64_t& q = acc[4 * (c / 8 + g) + i];
+              uint64_t& q = acc[4 * g + i];
               const uint32_t* v = t[i >> 1] + 4 * g + 2 * (i & 1);
-              q = fma2(pack2(v[0], v[1]), mul2(s, rw[i]), q);
+              q = fma2(pack2(v[0], v[1]), mul2(s[g], rw[i]), q);
             }
-          }
-        }
-        if (mine <= 0) {            // no columns: release the buffer at once
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&t_empty[buf]);
-        }
-        if (j == SG - 1 || kb == kb1 - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[slot]);
-          ++ns;
         }
       }
-      if (!ok || p.split > 1) break;
+      if (__any_sync(0xffffffffu, gave_up)) break;
+      if (p.split > 1) break;
       // eight columns at a time through the warp's own shared memory, so that a store covers 32 consecutive outputs
       const int o = quarter * 32 + lane;
       const int64_t n_out = (int64_t)tile * p.bn + o;
       const bool mine_out = o < p.bn && n_out < p.N;
-      const int m_cols = min(mine, p.M - c0);
-      float* tr = (float*)(sm + S::OFF_TR) + warp * TR_FLOATS;
+      const int m_cols = min(16, p.M - c0);
+      float* tr = (float*)(sm + OFF_TR) + warp * TR_FLOATS;
       int64_t off = (int64_t)c0 * p.ld_out + n_out;
 #pragma unroll
-      for (int g = 0; g < 2 * NC; ++g) {
+      for (int g = 0; g < 2; ++g) {
         if (8 * g >= m_cols) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -343,9 +354,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     float* part = (float*)sm;                               // [cols][PAD_N]: 128 outputs
     __syncthreads();
     if (warp < EPI_WARPS) {
-      const int c0 = (warp >> 2) * 16 * NC + 2 * (lane & 3), o = (warp & 3) * 32 + (lane >> 2);
+      const int c0 = (warp >> 2) * 16 + 2 * (lane & 3), o = (warp & 3) * 32 + (lane >> 2);
 #pragma unroll
-      for (int g = 0; g < 2 * NC; ++g)
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = unpack2(acc[4 * g + i]);
@@ -386,16 +397,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   }
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Params);
-
-Kernel pick(int nc) { return nc == 1 ? gemm_fp8_kernel<1> : gemm_fp8_kernel<2>; }
-int smem_bytes(int nc) { return nc == 1 ? Shape<1>::BYTES : Shape<2>::BYTES; }
-
-cudaLaunchConfig_t config(unsigned grid, int split, int nc, cudaStream_t st, cudaLaunchAttribute* attrs) {
+cudaLaunchConfig_t config(unsigned grid, int split, cudaStream_t st, cudaLaunchAttribute* attrs) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem_bytes(nc);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = st;
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
@@ -420,8 +426,8 @@ int resident_clusters(int split) {
   }
   int n = 0;
   cudaLaunchAttribute attrs[2];
-  cudaLaunchConfig_t cfg = config((unsigned)split, split, 2, 0, attrs);
-  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel<2>, &cfg) != cudaSuccess) {
+  cudaLaunchConfig_t cfg = config((unsigned)split, split, 0, attrs);
+  if (cudaOccupancyMaxActiveClusters(&n, (void*)gemm_fp8_kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();            // not a fault of the call: such clusters are not used
     n = 0;
   }
@@ -458,9 +464,11 @@ void choose_tiles(int64_t N, int cols, int kbs, int* bn, int* split) {
 
 }  // namespace gtc
 
-// Rows of a from which the pairs of CTAs take the call: 128 x 154880 x 6144 takes 182 us here and 218 there, and
-// this kernel's tile has at most 128 columns.
-constexpr int64_t kPairRows = 128;
+// Calls with more rows of a than this take the pairs of CTAs: 64 x 154880 x 6144 takes 153 us here and 190 there, 64 x
+// 6144 x 12288 24.5 and 27.0.  With tiles of 128 columns (32 per epilogue warp) this kernel took 196 us for 80 x 154880 x
+// 6144 and 209 for 128, the pairs 192 and 198; 128 x 2048 x 6144 11.5 against 13.3.
+constexpr int64_t kPairRows = 64;
+static_assert(kPairRows == gtc::COLS, "a tile holds every row of a");
 
 int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   using namespace gtc;
@@ -479,9 +487,8 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   p.M = (int)g.M; p.N = (int)g.N; p.kbs = (int)(g.K / KB);
   p.cols = (int)(ceil_div(g.M, 16) * 16);
   p.w_rows = g.w_scale_rows;
-  const int nc = (p.cols + 63) / 64;
-  static std::atomic<uint64_t> attr[2];
-  if (!set_smem_limit_once(pick(1), smem_bytes(1), attr[0]) || !set_smem_limit_once(pick(2), smem_bytes(2), attr[1])) {
+  static std::atomic<uint64_t> attr;
+  if (!set_smem_limit_once(gemm_fp8_kernel, SMEM_BYTES, attr)) {
     set_error("gemm_fp8_block128: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
   }
@@ -497,14 +504,14 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   p.status = g.status;
   CUtensorMap mw, ma;
   if (!make_tma_2d(&mw, 0, g.w, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, KB, (uint32_t)p.bn, true) ||
-                    !make_tma_2d(&ma, 0, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, KB, (uint32_t)p.cols, true)) {
+      !make_tma_2d(&ma, 0, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, KB, (uint32_t)p.cols, true)) {
     set_error("gemm_fp8_block128: cuTensorMapEncodeTiled failed");
     return MTPSD_ECUDA;
   }
   const unsigned grid = p.split > 1 ? (unsigned)(p.tiles * p.split) : (unsigned)std::min<int64_t>(p.tiles, num_sms());
   cudaLaunchAttribute attrs[2];
-  cudaLaunchConfig_t cfg = config(grid, p.split, nc, st, attrs);
-  cudaLaunchKernelEx(&cfg, pick(nc), mw, ma, p);
+  cudaLaunchConfig_t cfg = config(grid, p.split, st, attrs);
+  cudaLaunchKernelEx(&cfg, gemm_fp8_kernel, mw, ma, p);
   return check_launch("gemm_fp8_block128");
 }
 

@@ -14,12 +14,17 @@
 //
 // Roles (384 threads, one CTA per SM), as k_gemm_fp8.cu but:
 //   warps 0-7   epilogue: lanes 32 (w % 4) .. +31, of every 64 columns the 32 of half w / 4; 32 NP
-//               accumulators a thread (setmaxnreg moves the other warps' registers here: 200 against 104).
-//               Sixteen warps of half as many were slower (697 against 601 us at 768 x 154880 x 6144): a
-//               warp's waits and hand-offs cost about 130 instructions a block, whatever it adds.
+//               accumulators a thread (setmaxnreg moves the other warps' registers here: 208 against 88).
+//               Sixteen warps of half as many were slower (697 against 601 us at 768 x 154880 x 6144, before the
+//               scales were fetched ahead): a warp's waits and hand-offs cost the same whatever it adds.
 //   warp 8      TMA producer of this CTA's operands; both CTAs' copies complete on the leader's barrier.
 //   warp 9      TMEM allocation; in the leader (even) CTA the MMA issue for the pair.
 //   warp 10     scales of this CTA's rows of a;  warp 11  scales of the tile's weight rows.
+// What bounds it: 768 x 154880 x 6144 takes 586 us, 2.5 PFLOP/s: the tensor cores are busy half of the time, and an epilogue
+// warp's 950 cycles a block (eight reads of TMEM of 45, the fetch of the next scales and barrier 180, the hand-over of
+// the buffer and the first read's latency most of the rest) set the pace.  Handing the buffer over in two halves, so that
+// four are in flight, doubled the hand-overs and took 727 us; reads of 32 columns spilled (681 us).  Back to back on random
+// codes the GPU draws 1385 of its 1400 W (zeros: 755 W at the same speed), so that a shorter chain would give little.
 // With few tiles the blocks of K are split over up to 4 pairs of one cluster.
 #include <algorithm>
 
@@ -51,7 +56,7 @@ constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
 constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + alignment slack
-constexpr int EPI_REGS = 200, ROLE_REGS = 104;
+constexpr int EPI_REGS = 208, ROLE_REGS = 88;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 static_assert(ROWS * PART_LD * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
 // setmaxnreg shares out what the launch allots: 65536 / 384 threads, rounded down to 8
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap tmap_a,
                                                                    const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sm = smem_raw + (-saddr(smem_raw) & 1023u);     // no cast: loads stay loads of shared memory
   uint64_t* full = (uint64_t*)(sm + OFF_BAR);        // the leader's is used
   uint64_t* empty = full + NSTAGE;
   uint64_t* t_full = empty + NSTAGE;
@@ -200,31 +205,31 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
         }
       }
     } else if (warp == MMA_WARP && side == 0) {
-      int stage = 0, n = 0;
-      bool ok = true;
-      const uint32_t id = (1u << 4) | ((uint32_t)BN >> 3 << 17) | ((256u >> 4) << 24);   // M = 256, N = BN
-      const uint32_t mask = 3u << leader;
-      for (int tile = first; tile < p.tiles && ok; tile += step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          const int buf = n % NBUF, round = n / NBUF;
-          ok = wait_all_cluster(&full[stage], (n / NSTAGE) & 1, abort_flag, p.status);
-          if (ok && round > 0) ok = wait_all_cluster(&t_empty[buf], (round - 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t a_base = saddr(sm + stage * STAGE), b_base = a_base + HALF_BYTES;
+      if (elect_one()) {           // one thread waits and issues
+        int stage = 0, n = 0;
+        bool ok = true;
+        const uint32_t id = (1u << 4) | ((uint32_t)BN >> 3 << 17) | ((256u >> 4) << 24);   // M = 256, N = BN
+        const uint32_t mask = 3u << leader;
+        for (int tile = first; tile < p.tiles && ok; tile += step) {
+          for (int kb = kb0; kb < kb1; ++kb, ++n) {
+            const int buf = n % NBUF, round = n / NBUF;
+            ok = mbar::wait<true>(&full[stage], (n / NSTAGE) & 1, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+            if (ok && round > 0)
+              ok = mbar::wait<true>(&t_empty[buf], (round - 1) & 1, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = sw128_desc(saddr(sm + stage * STAGE));
             const uint32_t d = tmem_base + (uint32_t)(buf * COLS);
 #pragma unroll
-            for (int kk = 0; kk < KB / 32; ++kk)
-              mma_fp8_pair(d, sw128_desc(a_base + kk * 32), sw128_desc(b_base + kk * 32), id, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < KB / 32; ++kk)         // descriptors count 16 bytes
+              mma_fp8_pair(d, a + 2 * kk, a + (HALF_BYTES >> 4) + 2 * kk, id, kk > 0 ? 1u : 0u);
             mma_commit_pair(&t_full[buf], mask);
             mma_commit_pair(&empty[stage], mask);
+            if (++stage == NSTAGE) stage = 0;
           }
-          __syncwarp();
-          if (++stage == NSTAGE) stage = 0;
         }
+        mma_commit_pair(drain, mask);                    // every MMA has completed before TMEM is released
       }
-      if (elect_one()) mma_commit_pair(drain, mask);   // every MMA has completed before TMEM is released
       __syncwarp();
       volatile int dummy = 0;
       mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
@@ -296,33 +301,73 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
   // at(c) + 8 g + fc, +1, row 32 quarter + 8 i + fr (the 16x256b read of k_gemm_fp8.cu); else acc[8 c + i]: columns
   // at(c) + 2 i, +1, row 32 quarter + lane (the 32x32b read, twice as fast: 768 x 154880 x 6144 took 855 us with the other)
   uint64_t acc[8 * NP * PW];
+  // A wait that gave up makes the warp walk on without waiting, to the end, and store nothing: the blocks' loop then has
+  // no exit to test for.
+  bool gave_up = false;
+  auto finish = [&](uint64_t* bar, uint32_t parity) {               // of a wait whose first probe failed
+    if (!gave_up) gave_up = !mbar::wait<false>(bar, parity, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+  };
   {
-    int buf = 0, t_phase = 0, slot = 0, s_phase = 0;
-    bool ok = true;
+    int n = 0, slot = 0, s_phase = 0;             // blocks so far, scale slot
     const uint32_t te0 = map_rank(saddr(&t_empty[0]), leader);
     const uint32_t taddr0 = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c0;
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
+    for (int tile = first; tile < p.tiles; tile += step) {
       const int m_own = (tile % p.n_mt * 2 + (int)side) * ROWS + quarter * 32;    // the warp's first row of a
       const bool live = m_own < p.M;
 #pragma unroll
       for (int i = 0; i < 8 * NP * PW; ++i) acc[i] = 0ull;
-      for (int kb = kb0, j = 0; kb < kb1; ++kb) {
-        if (j == 0) ok = wait_all(&s_full[slot], s_phase, abort_flag, p.status);
-        if (!ok) break;
-        // every scale is read before the wait for the products: the chain of a block is what bounds this loop
+      // The scales of a block and the probe for its products are fetched while the block before is still being
+      // added: the chain of a block (waits, scales, reads of TMEM) is what bounds this loop.
+      float rs[4];
+      float4 w4;
+      const float* scw;
+      bool ready;
+      auto fetch = [&](int j, int block) {
         const float* sc = scales + slot * SLOT_FLOATS + j * ROWS + quarter * 32;
-        const float* scw = scales + slot * SLOT_FLOATS + SG * ROWS + j * (ROWS1 ? COLS : RUNS);
-        float rs[4], ws[4];
+        scw = scales + slot * SLOT_FLOATS + SG * ROWS + j * (ROWS1 ? COLS : RUNS);
         if constexpr (ROWS1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) rs[i] = sc[8 * i + fr];
         } else {
-          const float4 w = *(const float4*)scw;
-          const float r = sc[lane];
-          ws[0] = r * w.x; ws[1] = r * w.y; ws[2] = r * w.z; ws[3] = r * w.w;
+          w4 = *(const float4*)scw;
+          rs[0] = sc[lane];
         }
-        ok = wait_all(&t_full[buf], t_phase, abort_flag, p.status);
-        if (!ok) break;
+        ready = mbar::try_wait<false>(&t_full[block % NBUF], block / NBUF & 1);
+      };
+      auto next_slot = [&]() {
+        if (!mbar::try_wait<false>(&s_full[slot], s_phase)) finish(&s_full[slot], s_phase);
+        __syncwarp();
+      };
+      auto leave_slot = [&]() {                   // every lane has read its scales
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[slot]);
+        if (++slot == NSLOT) {
+          slot = 0;
+          s_phase ^= 1;
+        }
+      };
+      next_slot();
+      fetch(0, n);
+      for (int kb = kb0, j = 0; kb < kb1; ++kb, ++n) {
+        const int buf = n % NBUF;
+        const bool last = kb == kb1 - 1;
+        auto fetch_next = [&]() {
+          if (++j == SG || last) {
+            leave_slot();
+            j = 0;
+            if (last) return;
+            next_slot();
+          }
+          fetch(j, n + 1);
+        };
+        uint64_t ws[NP];
+        if constexpr (!ROWS1) {
+          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int i = 0; i < NP; ++i) ws[i] = pack2(make_float2(rs[0] * w[i], rs[0] * w[i]));
+        }
+        if (!ready) finish(&t_full[buf], n / NBUF & 1);
+        __syncwarp();
         tc_fence_after();
         const uint32_t taddr = taddr0 + (uint32_t)(buf * COLS);
         if (live) {
@@ -346,6 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
               tc_fence_before();
               __syncwarp();
               if (lane == 0) arrive_at(te0 + 8 * buf);
+              if constexpr (!ROWS1) fetch_next();
             }
             if constexpr (ROWS1) {
 #pragma unroll
@@ -359,30 +405,19 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
                 }
               }
             } else {
-              const uint64_t s = pack2(make_float2(ws[c / PW], ws[c / PW]));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) acc[8 * c + i] = fma2(pack2(t[c & 1][2 * i], t[c & 1][2 * i + 1]), s, acc[8 * c + i]);
+              for (int i = 0; i < 8; ++i)
+                acc[8 * c + i] = fma2(pack2(t[c & 1][2 * i], t[c & 1][2 * i + 1]), ws[c / PW], acc[8 * c + i]);
             }
           }
+          if constexpr (ROWS1) fetch_next();
         } else {
-          __syncwarp();
           if (lane == 0) arrive_at(te0 + 8 * buf);
-        }
-        if (++buf == NBUF) {
-          buf = 0;
-          t_phase ^= 1;
-        }
-        if (++j == SG || kb == kb1 - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[slot]);
-          j = 0;
-          if (++slot == NSLOT) {
-            slot = 0;
-            s_phase ^= 1;
-          }
+          fetch_next();
         }
       }
-      if (!ok || p.split > 1) break;
+      if (__any_sync(0xffffffffu, gave_up)) break;
+      if (p.split > 1) break;
       if (!live) continue;
       const int n_first = tile / p.n_mt * BN + c0;
       if constexpr (!ROWS1) {
