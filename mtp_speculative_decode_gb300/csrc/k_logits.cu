@@ -43,6 +43,7 @@ static_assert((int64_t)MAX_CHUNK * MAX_CLUSTER == 393216, "the vocabulary that t
 static_assert(MAX_CHUNK <= 65536, "list entries hold 16-bit positions");
 constexpr int LIST = 2048;                    // tokens with a table word in the list (with more, the bitmap is walked)
 constexpr int ENTRIES = 512;                  // drafts and biases put down in shared memory (more are read again)
+constexpr int REPEATS = 64;                   // entries of a row whose token another entry has too (with more, every entry counts as one)
 
 // shared memory: list, entries (position, word, bias), the two bitmaps, the row's mask, the logits or values
 constexpr int OFF_ENT = LIST * 4;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
   __shared__ Request R;
   __shared__ float s_red[WARPS];
   __shared__ unsigned s_idx;
-  __shared__ int s_dup, s_list, s_abort;
+  __shared__ int s_rep[REPEATS], s_reps, s_list, s_abort;
   __shared__ __align__(16) float4 s_peer[2][MAX_CLUSTER];   // (maximum, sum, position) of every CTA, by the row's parity
   __shared__ float4 s_row;                                  // the row's (maximum, sum, position)
   __shared__ __align__(8) uint64_t s_bar[2], s_in;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
     const bool special = nd + R.nb > 0;
     if (tid == 0) {
       s_idx = 0xffffffffu;
-      s_dup = 0;
+      s_reps = 0;
       if (r + 1 < r1 && bulk)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((uint64_t)source(r + 1)), "r"(bulk) : "memory");
     }
@@ -366,7 +367,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
       for (int e = tid; e < entries; e += THREADS) {
         const int c = position(e);
         if (c < 0) continue;
-        if (atomicOr(&marks[c >> 5], 1u << (c & 31)) >> (c & 31) & 1) s_dup = 1;
+        if (atomicOr(&marks[c >> 5], 1u << (c & 31)) >> (c & 31) & 1) {
+          const int i = atomicAdd(&s_reps, 1);
+          if (i < REPEATS) s_rep[i] = c;
+        }
         atomicOr(&skip[c >> 5], 1u << (c & 31));
       }
     }
@@ -432,8 +436,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
         for (int e = 0; e < G; e += 4)
           *(float4*)(xs + c + e) = make_float4(value8(e), value8(e + 1), value8(e + 2), value8(e + 3));
       }
-      if (out) {
-        if (p.vec_out && !sp && c + G <= len) {
+      if (out && p.vec_out) {
+        if (!sp && c + G <= len) {
 #pragma unroll
           for (int e = 0; e < G; e += 4)
             *(float4*)(out + c + e) = make_float4(value8(e), value8(e + 1), value8(e + 2), value8(e + 3));
@@ -460,9 +464,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
       }
     }
     rm_next = mask_at(mask_next);
-    if (rw || special) {
+    const bool later = out && !p.vec_out;              // out_logits rows that cannot be written 16 bytes at a time
+    if (rw || special || later) {
       __syncthreads();                                 // the stream's values are written
       auto value = [&](int c) { return keep ? xs[c] : staged(c); };
+      // consecutive threads write consecutive tokens (a thread's eight one by one: 76 us for 68 rows of 50001 from memory)
+      if (later)
+        for (int c = tid; c < len; c += THREADS)
+          if (!bit(skip, c)) out[c] = keep || open(c) ? value(c) : -INFINITY;
       if (rw) {
         const int n = s_list;
         if (n <= LIST) {
@@ -482,20 +491,43 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
         }
       }
       if (special) {
-        const bool scan = s_dup != 0;                  // a token with several entries is its first one's
-        for (int e = THREADS - 1 - tid; e < entries; e += THREADS) {     // from the last warps: the first have the list
+        const int reps = s_reps;
+        const bool all = reps > REPEATS;
+        auto word = [&](int e, int c) { return e < ENTRIES ? ent_word[e] : rw ? (uint32_t)rw[start + c] : 0u; };
+        auto bias = [&](int e) { return e < ENTRIES ? ent_bias[e] : R.bv[e - R.K]; };
+        for (int e = THREADS - 1 - tid; !all && e < entries; e += THREADS) {     // from the last warps: the first have the list
           const int c = position(e);
-          if (c < 0) continue;
-          bool again = false;
-          if (scan)
-            for (int k = 0; k < e; ++k) again = again || position(k) == c;
-          if (again) continue;
-          int extra = 0;
-          for (int k = 0; k < nd; ++k) extra += position(k) == c;
-          float x = penalise(&R, value(c), e < ENTRIES ? ent_word[e] : rw ? rw[start + c] : 0u, extra);
-          for (int k = scan ? R.K : max(e, R.K); k < (scan ? entries : e + 1); ++k)      // its biases, in order
-            if (position(k) == c) x = __fadd_rn(x, k < ENTRIES ? ent_bias[k] : R.bv[k - R.K]);
+          bool repeated = c < 0;
+          for (int i = 0; i < reps; ++i) repeated = repeated || s_rep[i] == c;
+          if (repeated) continue;
+          float x = penalise(&R, value(c), word(e, c), e < R.K ? 1 : 0);
+          if (e >= R.K) x = __fadd_rn(x, bias(e));
           single(c, x);
+        }
+        // a token with several entries: a warp looks through them (300 biases with one pair among them, a thread
+        // each through all of them: 70 us instead of 23 for the 68 rows of 50001)
+        auto candidate = [&](int i) { return all ? position(i) : s_rep[i]; };
+        for (int i = warp; i < (all ? entries : reps); i += WARPS) {
+          const int c = candidate(i);
+          bool again = c < 0;
+          for (int k = lane; k < i; k += 32) again = again || candidate(k) == c;
+          if (__any_sync(0xffffffffu, again)) continue;
+          int extra = 0, first = entries;
+          for (int k = lane; k < nd; k += 32)
+            if (position(k) == c) {
+              ++extra;
+              first = min(first, k);
+            }
+          extra = __reduce_add_sync(0xffffffffu, extra);
+          for (int k = R.K + lane; k < entries; k += 32)
+            if (position(k) == c) first = min(first, k);
+          first = __reduce_min_sync(0xffffffffu, first);
+          float x = penalise(&R, value(c), word(first, c), extra);
+          for (int k0 = R.K; k0 < entries; k0 += 32) {               // its biases, in order
+            uint32_t hit = __ballot_sync(0xffffffffu, k0 + lane < entries && position(k0 + lane) == c);
+            for (; hit; hit &= hit - 1) x = __fadd_rn(x, bias(k0 + __ffs(hit) - 1));
+          }
+          if (lane == 0) single(c, x);
         }
       }
     }
@@ -657,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
         __syncthreads();                               // the values are read and may be overwritten
         stage(r + 1, rm_next);
       } else {
-        __syncthreads();                               // s_idx and s_dup are read, the marks are cleared
+        __syncthreads();                               // s_idx and s_reps are read, the marks are cleared
       }
     }
   }
@@ -727,7 +759,7 @@ int launch_process_logits(const mtpsd_logits_args& a, cudaStream_t st) {
   p.vec_out = (uintptr_t)a.out_logits % 16 == 0 && a.out_ld % 4 == 0;
   p.vec_probs = (uintptr_t)a.probs % 16 == 0 && a.probs_ld % 4 == 0;
   const int smem = smem_bytes(p.chunk, per_token);
-  // few and short chunks: CTAs of 256 threads, so that more rows run at once (68 rows of 50001: 36 us with 512)
+  // few and short chunks: CTAs of 256 threads, so that more rows run at once (68 rows of 50001 took 29 us, with 512 36)
   const int n_cta = smem <= share(4) ? 4 : smem <= share(2) ? 2 : 1;
   const int threads = n_cta == 4 ? 256 : 512;
   static std::atomic<uint64_t> attr[4];

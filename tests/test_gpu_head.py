@@ -424,6 +424,27 @@ def test_logits_largest_vocabularies(mt, V):
     c.check(am, probs)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,n,tokens", [(5000, 300, 290), (5001, 300, 235), (5001, 300, 100), (1001, 700, 40), (64, 700, 1)])
+def test_logits_tokens_with_several_entries(mt, V, n, tokens, dtype):
+    """Biases of a token that other biases and drafts have too, few and many of them, are added in list order."""
+    rng = np.random.default_rng(n + tokens)
+    c = Case(V + n, 3, 5, V, dtype, counts=True, pen=True, bias=n, temp=True)
+    some = rng.permutation(V)[:tokens].astype(np.int32)
+    c.bias[1][:] = some[rng.integers(0, tokens, len(c.bias[1]))]
+    c.bias[1][:tokens] = some
+    c.draft[:] = some[rng.integers(0, tokens, c.draft.shape)]
+    c.draft[0, 3] = c.draft[0, 1]
+    argmax = torch.empty(c.R, dtype=torch.int64, device="cuda")
+    probs, out = torch.empty(c.R, V, device="cuda"), torch.empty(c.R, V, device="cuda")
+    for _ in range(2):                                 # the same bits again
+        before = out.clone()
+        c.call(mt, argmax=argmax, probs=probs, out_logits=out)
+        c.check(argmax, probs, out)
+    assert torch.equal(before, out)
+    c.check(c.call(mt))                                # nothing kept but the greedy token
+
+
 def test_logits_argmax_only_and_default(mt):
     c = Case(1, 4, 3, 3000, torch.bfloat16, **ALL)
     c.check(c.call(mt))
