@@ -121,9 +121,10 @@ __device__ __noinline__ float penalise(const Request* r, float x, uint32_t w, in
   return x;
 }
 
-// THREADS: 512 with two CTAs per SM, or 256 with four for short chunks.
+// THREADS: 384 with two CTAs per SM (a row's reductions and barriers cost every warp the same: 768 rows of 154880, argmax
+// only, take 104 us, with 512 threads 112 and with 256 120), or 256 with four for short chunks.
 template <bool BF16, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logits_kernel(const __grid_constant__ Params p) {
   constexpr int WARPS = THREADS / 32;
   constexpr int G = 8;                    // tokens per thread and step: a byte of each bitmap
   constexpr int ES = BF16 ? 2 : 4;
@@ -269,19 +270,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
         const int64_t row = a.count_rows ? a.count_rows[b + 1] : b + 1;
         if (row >= 0 && row < a.counts_rows) next_word = (const uint16_t*)a.counts + row * a.counts_ld;
       }
-      for (int e = tid; e < entries; e += THREADS) {
-        const int64_t t = e < R.K ? R.draft[e] : (int64_t)R.bt[e - R.K], c = t - start;
-        const bool in = c >= 0 && c < len;
-        if ((t < 0 || t >= a.V) && rank == 0) flag_status(a.dev_status, MTPSD_STATUS_INDEX_RANGE);
-        if (e < ENTRIES) {
-          ent_pos[e] = in ? (int)c : -1;
-          ent_word[e] = in && w ? w[t] : 0u;
-          ent_bias[e] = e < R.K ? 0.f : R.bv[e - R.K];
-        }
-      }
+      auto token = [&](int e) { return e < R.K ? R.draft[e] : (int64_t)R.bt[e - R.K]; };
+      const int64_t t0 = tid < entries ? token(tid) : 0;     // on its way during the scan
       if (w) {
         // eight words per thread and step: one byte of the bitmap (a row's words reach past V to a multiple of 8)
-        constexpr int U = 4;
+        constexpr int U = 5;
         for (int g0 = tid; g0 - lane < (len + 7) / 8; g0 += U * THREADS) {
           uint4 k[U];
           uint32_t nz[U];
@@ -330,6 +323,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) process_logits_kernel
       }
       else {
         for (int i = tid; i < p.chunk / 32; i += THREADS) skip[i] = 0;
+      }
+      for (int e = tid; e < entries; e += THREADS) {
+        const int64_t t = e == tid ? t0 : token(e), c = t - start;
+        const bool in = c >= 0 && c < len;
+        if ((t < 0 || t >= a.V) && rank == 0) flag_status(a.dev_status, MTPSD_STATUS_INDEX_RANGE);
+        if (e < ENTRIES) {
+          ent_pos[e] = in ? (int)c : -1;
+          ent_word[e] = in && w ? w[t] : 0u;
+          ent_bias[e] = e < R.K ? 0.f : R.bv[e - R.K];
+        }
       }
     }
     const uint16_t* const rw = R.word;
@@ -759,12 +762,12 @@ int launch_process_logits(const mtpsd_logits_args& a, cudaStream_t st) {
   p.vec_out = (uintptr_t)a.out_logits % 16 == 0 && a.out_ld % 4 == 0;
   p.vec_probs = (uintptr_t)a.probs % 16 == 0 && a.probs_ld % 4 == 0;
   const int smem = smem_bytes(p.chunk, per_token);
-  // few and short chunks: CTAs of 256 threads, so that more rows run at once (68 rows of 50001 took 29 us, with 512 36)
+  // few and short chunks: CTAs of 256 threads, so that more rows run at once (68 rows of 50001 took 29 us, with two of 512 36)
   const int n_cta = smem <= share(4) ? 4 : smem <= share(2) ? 2 : 1;
-  const int threads = n_cta == 4 ? 256 : 512;
+  const int threads = n_cta == 4 ? 256 : 384;
   static std::atomic<uint64_t> attr[4];
-  Kernel kern = bf16 ? (threads == 256 ? process_logits_kernel<true, 256> : process_logits_kernel<true, 512>)
-                     : (threads == 256 ? process_logits_kernel<false, 256> : process_logits_kernel<false, 512>);
+  Kernel kern = bf16 ? (threads == 256 ? process_logits_kernel<true, 256> : process_logits_kernel<true, 384>)
+                     : (threads == 256 ? process_logits_kernel<false, 256> : process_logits_kernel<false, 384>);
   if (!set_smem_limit_once(kern, smem_bytes(MAX_CHUNK, 4), attr[2 * bf16 + (threads == 256)])) {
     set_error("process_logits: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
