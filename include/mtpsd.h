@@ -454,7 +454,7 @@ int mtpsd_topk_share_gather(const int32_t* step0_topk, const uint32_t* row_offse
  *   out [M, N], out_dtype MTPSD_BF16 or MTPSD_F32, row stride ld_out (elements, >= N)
  * Each block's sum and the sum over the blocks are held in float32; the result is rounded
  * once to out_dtype.  The order of the sums depends on M, N and K only.
- * K is a multiple of 128; a and w are 16-byte aligned, out to its element; M, N < 2^31.
+ * K is a multiple of 128; a and w are 16-byte aligned, out to its element; M, N <= 2^31 - 256.
  * M = 0 or N = 0 launches nothing; K = 0 writes zeros.  A NaN code (0x7F, 0xFF) or a scale that is
  * not finite reaches the outputs of its own row m and column n and no others.
  */
@@ -478,8 +478,8 @@ int64_t mtpsd_token_counts_ld(int64_t V);   /* V rounded up to 8 */
 /* Builds the rows of B requests from their tokens (the rows' old contents are dropped; columns V .. ld - 1
  * become 0):
  *   tokens [S] int64, request b's are tokens[offsets[b] .. offsets[b+1]-1] (offsets uint32 [B+1], the
- *   prefix sums of mtpsd_merge_tokens); its first n_prompt[b] (int64 [B]; NULL: all of them) are the
- *   prompt, the others output.
+ *   prefix sums of mtpsd_merge_tokens); its first n_prompt[b] (int64 [B], cut to 0 .. its tokens; NULL: all
+ *   of them) are the prompt, the others output.
  * Offsets past S are cut to S and flagged MTPSD_STATUS_ROW_RANGE; a segment that ends before it starts is empty. */
 int mtpsd_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* offsets, const int64_t* n_prompt,
                              int32_t B, int64_t V, int16_t* counts, int64_t ld, int32_t n_rows,
@@ -513,7 +513,8 @@ int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted,
  * row_offsets[0] .. row_offsets[B]-1 (a padded batch) are left as they were.
  * Bad device values are skipped and flagged: draft and bias tokens outside [0, V) and bias offsets past
  * n_bias MTPSD_STATUS_INDEX_RANGE; count_rows (as the token table; -1: nothing counted) and mask_rows (-1: no mask)
- * outside their arrays MTPSD_STATUS_ROW_RANGE.  V <= 393216.
+ * outside their arrays and a row_offsets[B] past R (cut to it) MTPSD_STATUS_ROW_RANGE.  V <= 393216,
+ * K + n_bias < 2^31.  Apart from out_logits = logits no output may overlap an input.
  */
 typedef struct {
   int32_t B;                   /* requests */

@@ -417,8 +417,9 @@ int mtpsd_gemm_fp8_block128(const uint8_t* a, const float* a_scale, const uint8_
                             int32_t w_scale_rows, int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* out,
                             int64_t ld_out, int32_t* dev_status, void* stream) {
   g_err[0] = 0;
-  if (M < 0 || N < 0 || K < 0 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
-    return fail(MTPSD_EINVAL, "gemm_fp8_block128: M, N and K must be in 0..2^31-1");
+  // a tile's last row is a 32-bit number too
+  if (M < 0 || N < 0 || K < 0 || M > 0x7fffff00LL || N > 0x7fffff00LL || K > 0x7fffffffLL)
+    return fail(MTPSD_EINVAL, "gemm_fp8_block128: M and N must be in 0..2^31-256, K in 0..2^31-1");
   if (K % 128) return fail(MTPSD_EUNSUPPORTED, "gemm_fp8_block128: K must be a multiple of 128");
   if (w_scale_rows != 1 && w_scale_rows != 128) return fail(MTPSD_EUNSUPPORTED, "gemm_fp8_block128: w_scale_rows must be 1 or 128");
   if (out_dtype != MTPSD_BF16 && out_dtype != MTPSD_F32)
@@ -494,6 +495,8 @@ int mtpsd_process_logits(const mtpsd_logits_args* a, void* stream) {
                               "process_logits")) return rc;
   if (a->bias_offsets && (a->n_bias < 0 || (a->n_bias > 0 && (!a->bias_tokens || !a->bias_values))))
     return fail(MTPSD_EINVAL, "process_logits: biases need n_bias >= 0, bias_tokens and bias_values");
+  if (a->bias_offsets && (int64_t)a->K + a->n_bias > 0x7fffffffLL)
+    return fail(MTPSD_EINVAL, "process_logits: need K + n_bias < 2^31");
   if (a->bitmask && (a->n_masks < 0 || (!a->mask_rows && a->n_masks < a->R)))
     return fail(MTPSD_EINVAL, "process_logits: fewer masks than rows");
   if (a->R == 0) return MTPSD_OK;

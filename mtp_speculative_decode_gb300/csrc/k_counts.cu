@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(BUILD_THREADS, 1) token_counts_build_kernel(
   const int64_t first = offsets[b], stop = offsets[b + 1], end = min(stop, S);
   if (first_cta && tid == 0 && stop > S) flag_status(status, MTPSD_STATUS_ROW_RANGE);
   if (row < 0) return;           // the whole cluster
-  const int64_t n = max(end - first, (int64_t)0), cut = n_prompt ? first + n_prompt[b] : end;
+  const int64_t n = max(end - first, (int64_t)0), cut = n_prompt ? first + min(max(n_prompt[b], (int64_t)0), n) : end;
   const int64_t j0 = first + n * part / parts, j1 = first + n * (part + 1) / parts;
   const int64_t base = (int64_t)which * range;
   __syncthreads();

@@ -223,6 +223,16 @@ def test_table_build(mt, lens, V, prompt):
     assert np.array_equal(table.cpu().numpy(), want)
 
 
+def test_table_prompt_lengths_past_the_tokens(mt):
+    """Prompt lengths outside 0 .. the request's tokens are cut to that range."""
+    V, toks = 50, np.arange(40, dtype=np.int64)
+    off = np.array([0, 7, 7, 20, 40], np.uint32)
+    big = np.iinfo(np.int64)
+    want = ologits.token_counts_build(np.zeros((4, 56), np.int16), toks, off, V, [0, 0, 13, 20])
+    got = mt.token_counts_build(dev(toks), u32(off), V, n_prompt=dev(np.array([big.min, -1, 13, big.max], np.int64)))
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_table_build_saturates(mt):
     V = 40
     tok = np.array([3] * 40000 + [4] * 32767 + [5] * 32766 + [2] * 7, np.int64)

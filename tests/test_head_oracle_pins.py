@@ -119,7 +119,7 @@ def test_gemm_refusals(native):
     f = native.lib().mtpsd_gemm_fp8_block128
     E, U = native.MTPSD_EINVAL, native.MTPSD_EUNSUPPORTED
     ok = dict(a=16, sa=16, w=16, sw=16, rows=1, M=4, N=8, K=256, dt=native.MTPSD_BF16, out=16, ld=8)
-    for change, code in ((dict(M=-1), E), (dict(N=1 << 31), E), (dict(K=64), U), (dict(rows=2), U),
+    for change, code in ((dict(M=-1), E), (dict(N=1 << 31), E), (dict(M=(1 << 31) - 255), E), (dict(K=64), U), (dict(rows=2), U),
                          (dict(dt=native.MTPSD_FP8_E4M3), U), (dict(ld=7), E), (dict(a=None), E), (dict(sw=None), E),
                          (dict(out=None), E), (dict(a=8), E), (dict(w=17), E), (dict(out=17), E),
                          (dict(out=18, dt=native.MTPSD_F32), E), (dict(sa=18), E)):
@@ -158,6 +158,7 @@ def test_process_refusals(native):
                          (dict(counts=16, counts_ld=40, counts_rows=1), E),
                          (dict(counts=8, counts_ld=40, counts_rows=2), E),
                          (dict(bias_offsets=8, n_bias=-1), E), (dict(bias_offsets=8, n_bias=3), E),
+                         (dict(bias_offsets=8, bias_tokens=8, bias_values=8, n_bias=(1 << 31) - 1, K=1, draft=8), E),
                          (dict(bitmask=8, n_masks=3), E), (dict(bitmask=8, n_masks=-1, mask_rows=8), E),
                          (dict(logits=18), E), (dict(probs=18, probs_ld=40), E),
                          (dict(out_logits=16, out_ld=48), E),                                  # in place, other stride
