@@ -13,7 +13,7 @@
 // 16 (operand B), so the few rows of a cost only as much as there are of them
 // and the weight streams through once.  A tile is `bn` <= 128 outputs: the weight
 // read bounds these calls (16 x 154880 x 6144 runs at 98 % of the measured copy
-// rate, 144 us; 64 rows at 94 %, 153 us), so bn is chosen such that the tiles load every SM alike; TMEM lanes
+// rate, 144 us; 64 rows at 96 %, 150 us), so bn is chosen such that the tiles load every SM alike; TMEM lanes
 // past bn hold products of stale operands and are not stored.
 //
 // The epilogue reads TMEM (lane = output, column = row of a) in the 16x256b
@@ -23,16 +23,19 @@
 // shared-memory cycles than the MMAs' operands, 290 against 186 us without them
 // at 192 x 154880 x 6144.)
 //
+// A warp's chain of waits and reads for a block takes about 1000 cycles, more than the block's bytes where a call has
+// few tiles.  So the epilogue warps form 2 or 4 sets, of which set i takes the blocks with (block of K) % sets = i and adds
+// for itself; at the end of a tile the sets' sums are added in order.  For the same reason one thread each issues the
+// copies and the MMAs, instead of a warp that waits and votes.  64 x 6144 x 12288: 25.0 us with one set, 22.6 with two, 19.7
+// with single threads; 16 x 6144 x 12288 22.8, 20.0 and 17.1; 64 x 154880 x 6144 158, 152 and 150.
+//
 // Roles (608 threads, one CTA per SM):
-//   warps 0-15  epilogue: warp w takes the TMEM lanes 32 (w % 4) .. +31 and the columns of quarter w / 4
-//               (four warps per scheduler hide the latency of the TMEM reads).  A block's scales and the probe
-//               of its barrier are fetched before the block in front is added: read after the wait, they made
-//               the chain of a block long enough to show (163 us at 64 x 154880 x 6144).
+//   warps 0-15  epilogue: warp w takes the TMEM lanes 32 (w % 4) .. +31 and, of set (w / 4) % sets, 32 columns.
 //   warp 16     TMA producer: a ring of stages of one block (128 x 128 bytes of w, cols x 128 of a).
 //   warp 17     TMEM allocation and MMA issue.
 //   warp 18     scales: a ring of slots of four blocks' scales of the rows of a and of the weight rows.
 // With few tiles the blocks of K of a tile are split over a cluster of up to 8 CTAs (consecutive
-// runs of blocks), which add their accumulators through distributed shared memory in rank order.
+// runs of blocks), which add their sums through distributed shared memory in rank order.
 // The order of every sum is fixed by the sizes and the device.  Every mbarrier wait is bounded
 // (2 s): on expiry the kernel flags MTPSD_STATUS_WAIT_TIMEOUT, drains its copies, frees TMEM and returns.
 #include <algorithm>
@@ -49,22 +52,19 @@ constexpr int THREADS = 32 * 19;
 constexpr int MAX_SPLIT = 8;
 constexpr int W_BYTES = TILE_N * KB;
 constexpr int PAD_N = TILE_N + 4;         // row stride (floats) of a partial tile: a fragment's four columns miss each other's banks
-constexpr int TR_LD = 36;                 // the same for the transposed store of 8 columns x 32 outputs
-constexpr int TR_FLOATS = 8 * TR_LD;     // per epilogue warp
 
-constexpr int COLS = 64;                  // most columns (rows of a) of a tile; 16 per epilogue warp
+constexpr int COLS = 64;                  // most columns (rows of a) of a tile
 constexpr int STAGE = W_BYTES + COLS * KB;
-constexpr int NSTAGE = 192 * 1024 / STAGE;
+constexpr int NSTAGE = 6;
 constexpr int NBUF = TMEM_COLS / COLS;
 constexpr int SLOT_FLOATS = SG * (COLS + TILE_N);
 constexpr int OFF_SCALE = NSTAGE * STAGE;
-constexpr int OFF_TR = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;
-constexpr int OFF_BAR = OFF_TR + EPI_WARPS * TR_FLOATS * 4;
+constexpr int OFF_PART = OFF_SCALE + NSLOT * SLOT_FLOATS * 4;     // the sets' accumulators: 2 x 64 or 4 x 32 columns
+constexpr int OFF_BAR = OFF_PART + 2 * COLS * PAD_N * 4;
 constexpr int N_BARS = 2 * NSTAGE + 2 * NBUF + 2 * NSLOT + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;         // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert(COLS * PAD_N * 4 <= NSTAGE * STAGE, "the partial tile fits the stage ring");
 static_assert(OFF_BAR % 16 == 0, "barriers are aligned");
 
 struct Params {
@@ -77,14 +77,33 @@ struct Params {
   int bn, tiles;          // outputs of a tile, tiles
   int w_rows;             // weight rows that share a scale: 1 or 128
   int split;              // CTAs per cluster
+  int sets;               // sets of epilogue warps: 4 (up to 32 columns) or 2
   int out_f32;
+  int vec_out;            // four consecutive outputs of a row can be stored at once
   int vec_scales;         // a block row's scales can be read four at a time
   int32_t* status;
 };
 
-__device__ __forceinline__ void store_out(const Params& p, int64_t off, float v) {
-  if (p.out_f32) ((float*)p.out)[off] = v;
-  else ((__nv_bfloat16*)p.out)[off] = __float2bfloat16_rn(v);
+// Outputs o .. o + 3 of a tile for row m of a.
+__device__ __forceinline__ void store4(const Params& p, int m, int tile, int o, float4 v) {
+  const int64_t n = (int64_t)tile * p.bn + o, off = (int64_t)m * p.ld_out + n;
+  const int left = (int)min((int64_t)(p.bn - o), p.N - n);
+  if (left >= 4 && p.vec_out) {
+    if (p.out_f32) {
+      *(float4*)((float*)p.out + off) = v;
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      *(uint2*)((__nv_bfloat16*)p.out + off) = make_uint2(*(const uint32_t*)&lo, *(const uint32_t*)&hi);
+    }
+    return;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) {
+      if (p.out_f32) ((float*)p.out)[off + i] = e[i];
+      else ((__nv_bfloat16*)p.out)[off + i] = __float2bfloat16_rn(e[i]);
+    }
 }
 
 __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_w,
@@ -111,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
     }
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(&t_full[i], 1);
-      mbar_init(&t_empty[i], EPI_WARPS);
+      mbar_init(&t_empty[i], EPI_WARPS / p.sets);
     }
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(&s_full[i], 1);
@@ -141,59 +160,58 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
   const int first = (int)blockIdx.x / p.split, step = (int)gridDim.x / p.split;   // this cluster's tiles
   const int kb0 = (int)((int64_t)rank * p.kbs / p.split), kb1 = (int)((int64_t)(rank + 1) * p.kbs / p.split);
-  // acc[4 j + 2 h + i]: columns 8 j + 2 (lane % 4), +1 of the warp's, output 16 h + 8 i + lane / 4 of its 32
-  uint64_t acc[8];
+  float* part = (float*)(sm + OFF_PART);     // [sets][128 / sets columns][PAD_N]: 128 outputs
 
   if (warp == PRODUCER_WARP) {
-    int n = 0;
-    bool ok = true;
-    const uint32_t bytes = (uint32_t)((p.bn + p.cols) * KB);
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const int n0 = tile * p.bn;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int stage = n % NSTAGE, round = n / NSTAGE;
-        if (round > 0) ok = wait_all(&empty[stage], (round - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        if (elect_one()) {
+    if (elect_one()) {             // one thread waits and copies
+      int n = 0, stage = 0;
+      bool ok = true;
+      const uint32_t bytes = (uint32_t)((p.bn + p.cols) * KB);
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const int n0 = tile * p.bn;
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          if (n >= NSTAGE)
+            ok = mbar::wait<false>(&empty[stage], (n / NSTAGE - 1) & 1, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+          if (!ok) break;
           const uint32_t dst = saddr(sm + stage * STAGE);
           mbar_expect_tx(&full[stage], bytes);
           tma_load_2d(dst, &tmap_w, kb * KB, n0, &full[stage]);
           tma_load_2d(dst + W_BYTES, &tmap_a, kb * KB, 0, &full[stage]);
+          if (++stage == NSTAGE) stage = 0;
         }
-        __syncwarp();
       }
-    }
-    if (*abort_flag && lane == 0) {   // drain this CTA's copies still in flight (bounded)
-      volatile int dummy = 0;
-      for (int s = 0; s < NSTAGE; ++s) {
-        const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);   // loads of stage s
-        if (issued > 0) mbar::wait<false>(&full[s], (issued - 1) & 1, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
+      if (*abort_flag) {           // drain this CTA's copies still in flight (bounded)
+        volatile int dummy = 0;
+        for (int s = 0; s < NSTAGE; ++s) {
+          const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);   // loads of stage s
+          if (issued > 0) mbar::wait<false>(&full[s], (issued - 1) & 1, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
+        }
       }
     }
   } else if (warp == MMA_WARP) {
-    int n = 0;
-    bool ok = true;
-    const uint32_t id = idesc_n(p.cols);
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const int stage = n % NSTAGE, buf = n % NBUF, round = n / NBUF;
-        ok = wait_all(&full[stage], (n / NSTAGE) & 1, abort_flag, p.status);
-        if (ok && round > 0) ok = wait_all(&t_empty[buf], (round - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t w_base = saddr(sm + stage * STAGE), a_base = w_base + W_BYTES;
+    if (elect_one()) {             // one thread waits and issues
+      int n = 0, stage = 0;
+      bool ok = true;
+      const uint32_t id = idesc_n(p.cols);
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          const int buf = n % NBUF, round = n / NBUF;
+          ok = mbar::wait<false>(&full[stage], (n / NSTAGE) & 1, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+          if (ok && round > 0)
+            ok = mbar::wait<false>(&t_empty[buf], (round - 1) & 1, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t w = sw128_desc(saddr(sm + stage * STAGE));    // descriptors count 16 bytes
           const uint32_t d = tmem_base + (uint32_t)(buf * COLS);
 #pragma unroll
-          for (int kk = 0; kk < KB / 32; ++kk)
-            mma_fp8(d, sw128_desc(w_base + kk * 32), sw128_desc(a_base + kk * 32), id, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < KB / 32; ++kk) mma_fp8(d, w + 2 * kk, w + (W_BYTES >> 4) + 2 * kk, id, kk > 0 ? 1u : 0u);
           mma_commit(&t_full[buf]);
           mma_commit(&empty[stage]);
+          if (++stage == NSTAGE) stage = 0;
         }
-        __syncwarp();
       }
+      mma_commit(drain);           // every MMA has completed before TMEM is released
     }
-    if (elect_one()) mma_commit(drain);   // every MMA has completed before TMEM is released
     __syncwarp();
     volatile int dummy = 0;
     mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
@@ -245,146 +263,115 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_kernel(const __grid_const
       }
     }
   } else {
-    const int quarter = warp & 3, c0 = (warp >> 2) * 16;           // this warp's TMEM lanes and first column
+    const int quarter = warp & 3, set = (warp >> 2) % p.sets;      // this warp's TMEM lanes and set
+    const int c0 = 32 * ((warp >> 2) / p.sets), cols_set = 2 * COLS / p.sets;      // first column, columns of a set's tile
     const int fr = lane >> 2, fc = 2 * (lane & 3);                 // fragment row and column of this lane
-    const bool mine = c0 < p.cols;                                 // the warp has columns
-    int n = 0, slot = 0, s_phase = 0;                              // blocks so far, scale slot
-    // A wait that gave up makes the warp walk on without waiting, to the end, and store nothing: the blocks' loop then
-    // has no exit to test for.
+    const int nb = kb1 - kb0;
+    int n = 0, slot = 0, s_phase = 0;                              // blocks of the tiles so far, scale slot
+    // A wait that gave up makes the warp walk on without waiting, to the end: every warp comes to every barrier below.
     bool gave_up = false;
-    auto finish = [&](uint64_t* bar, uint32_t parity) {            // of a wait whose first probe failed
-      if (!gave_up) gave_up = !mbar::wait<false>(bar, parity, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar::try_wait<false>(bar, parity) && !gave_up)
+        gave_up = !mbar::wait<false>(bar, parity, abort_flag, p.status, mbar::DEFAULT_LIMIT_NS);
+      __syncwarp();
     };
-    for (int tile = first; tile < p.tiles; tile += step) {
+    auto epilogue_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory"); };
+    for (int tile = first; tile < p.tiles; tile += step, n += nb) {
+      // acc[8 q + 4 j + i]: columns 16 q + 8 j + fc, +1 of the warp's 32, output 8 i + fr of its 32
+      uint64_t acc[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0ull;
-      // The scales of a block and the probe for its products are fetched while the block before is still being added
-      float wr[4];                                                 // of the thread's four outputs
-      uint64_t cs[2];                                              // of its columns
-      bool ready;
-      auto fetch = [&](int j, int block) {
-        const float* sc = scales + slot * SLOT_FLOATS + j * COLS + c0 + fc;
-        const float* sr = scales + slot * SLOT_FLOATS + SG * COLS + j * TILE_N + quarter * 32 + fr;
+      for (int i = 0; i < 16; ++i) acc[i] = 0ull;
+      for (int b0 = 0; b0 < nb; b0 += SG) {
+        wait(&s_full[slot], s_phase);
+        for (int j = set; j < SG && b0 + j < nb; j += p.sets) {    // SG is a multiple of the sets
+          const int block = n + b0 + j, buf = block % NBUF;
+          const float* sc = scales + slot * SLOT_FLOATS + j * COLS + c0 + fc;
+          const float* sr = scales + slot * SLOT_FLOATS + SG * COLS + j * TILE_N + quarter * 32 + fr;
+          uint64_t rw[4];                                          // the weight scales of the thread's four outputs, twice each
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wr[i] = sr[8 * i];
-        cs[0] = *(const uint64_t*)sc;
-        cs[1] = *(const uint64_t*)(sc + 8);
-        ready = mbar::try_wait<false>(&t_full[block % NBUF], block / NBUF & 1);
-      };
-      auto next_slot = [&]() {
-        if (!mbar::try_wait<false>(&s_full[slot], s_phase)) finish(&s_full[slot], s_phase);
-        __syncwarp();
-      };
-      next_slot();
-      fetch(0, n);
-      for (int kb = kb0, j = 0; kb < kb1; ++kb, ++n) {
-        const int buf = n % NBUF;
-        uint64_t rw[4];
-        const uint64_t s[2] = {cs[0], cs[1]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rw[i] = pack2(make_float2(wr[i], wr[i]));
-        if (!ready) finish(&t_full[buf], n / NBUF & 1);
-        __syncwarp();
-        tc_fence_after();
-        uint32_t t[2][8];
-        if (mine) {
+          for (int i = 0; i < 4; ++i) rw[i] = pack2(make_float2(sr[8 * i], sr[8 * i]));
+          wait(&t_full[buf], block / NBUF & 1);
+          tc_fence_after();
           const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * COLS + c0);
-          tmem_ld_x2(taddr, t[0]);
-          tmem_ld_x2(taddr + (16u << 16), t[1]);
+          uint32_t t[2][16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (c0 + 16 * q < p.cols) {
+              tmem_ld_x2(taddr + 16 * q, t[q]);
+              tmem_ld_x2(taddr + (16u << 16) + 16 * q, t[q] + 8);
+            }
           tmem_ld_wait();
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&t_empty[buf]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (c0 + 16 * q < p.cols) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint64_t s = *(const uint64_t*)(sc + 16 * q + 8 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t* v = t[q] + 8 * (i >> 1) + 4 * g + 2 * (i & 1);
+                  acc[8 * q + 4 * g + i] = fma2(pack2(v[0], v[1]), mul2(s, rw[i]), acc[8 * q + 4 * g + i]);
+                }
+              }
+            }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&t_empty[buf]);
-        if (++j == SG || kb == kb1 - 1) {                          // every lane has read the slot's scales
-          if (lane == 0) mbar_arrive(&s_empty[slot]);
-          j = 0;
-          if (++slot == NSLOT) {
-            slot = 0;
-            s_phase ^= 1;
-          }
-          if (kb < kb1 - 1) next_slot();
+        if (lane == 0) mbar_arrive(&s_empty[slot]);                // every lane has read the slot's scales
+        if (++slot == NSLOT) {
+          slot = 0;
+          s_phase ^= 1;
         }
-        if (kb < kb1 - 1) fetch(j, n + 1);
-        if (mine) {
+      }
+      // ---- the sets' sums, in order, by all epilogue warps: a column at a time, four outputs per thread
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (c0 + 16 * q < p.cols) {
 #pragma unroll
           for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint64_t& q = acc[4 * g + i];
-              const uint32_t* v = t[i >> 1] + 4 * g + 2 * (i & 1);
-              q = fma2(pack2(v[0], v[1]), mul2(s[g], rw[i]), q);
+              const float2 v = unpack2(acc[8 * q + 4 * g + i]);
+              float* d = part + (set * cols_set + c0 + 16 * q + 8 * g + fc) * PAD_N + quarter * 32 + 8 * i + fr;
+              d[0] = v.x;
+              d[PAD_N] = v.y;
             }
         }
+      epilogue_barrier();
+      for (int c = warp; c < p.M; c += EPI_WARPS) {
+        float4 sum = *(const float4*)(part + c * PAD_N + 4 * lane);
+        for (int k = 1; k < p.sets; ++k) {
+          const float4 v = *(const float4*)(part + (k * cols_set + c) * PAD_N + 4 * lane);
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        if (p.split > 1) *(float4*)(part + c * PAD_N + 4 * lane) = sum;
+        else if (!gave_up) store4(p, c, tile, 4 * lane, sum);
       }
-      if (__any_sync(0xffffffffu, gave_up)) break;
       if (p.split > 1) break;
-      // eight columns at a time through the warp's own shared memory, so that a store covers 32 consecutive outputs
-      const int o = quarter * 32 + lane;
-      const int64_t n_out = (int64_t)tile * p.bn + o;
-      const bool mine_out = o < p.bn && n_out < p.N;
-      const int m_cols = min(16, p.M - c0);
-      float* tr = (float*)(sm + OFF_TR) + warp * TR_FLOATS;
-      int64_t off = (int64_t)c0 * p.ld_out + n_out;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (8 * g >= m_cols) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = unpack2(acc[4 * g + i]);
-          tr[fc * TR_LD + 8 * i + fr] = v.x;
-          tr[(fc + 1) * TR_LD + 8 * i + fr] = v.y;
-        }
-        __syncwarp();
-        if (mine_out) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (8 * g + e < m_cols) store_out(p, off + e * p.ld_out, tr[e * TR_LD + lane]);
-        }
-        off += 8 * p.ld_out;
-        __syncwarp();
-      }
+      epilogue_barrier();            // the sums are read before the next tile's are written
     }
   }
 
   __syncwarp();
   if (p.split > 1) {
-    // The cluster's one tile: every rank's accumulators into its own stage ring (its copies and MMAs are
-    // done: the epilogue has seen the last block), then each rank sums a part of the columns over the ranks.
-    float* part = (float*)sm;                               // [cols][PAD_N]: 128 outputs
-    __syncthreads();
-    if (warp < EPI_WARPS) {
-      const int c0 = (warp >> 2) * 16 + 2 * (lane & 3), o = (warp & 3) * 32 + (lane >> 2);
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = unpack2(acc[4 * g + i]);
-          part[(c0 + 8 * g) * PAD_N + o + 8 * i] = v.x;
-          part[(c0 + 8 * g + 1) * PAD_N + o + 8 * i] = v.y;
-        }
-    }
+    // The cluster's one tile: each rank sums a part of the columns over the ranks, in order.
     cluster_sync();
     if (warp < EPI_WARPS) {
       const int r0 = rank * p.M / p.split, r1 = (rank + 1) * p.M / p.split;
-      const int o = 4 * lane;                              // this thread's four outputs of a column
-      const int n_first = first * p.bn, n_end = min(p.N, n_first + p.bn);
       for (int c = r0 + warp; c < r1; c += EPI_WARPS) {
         float4 v[MAX_SPLIT];                               // every remote read in flight at once
 #pragma unroll
         for (int r = 0; r < MAX_SPLIT; ++r)
-          v[r] = r < p.split ? ld_cluster4(saddr(part + c * PAD_N + o), r) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[r] = r < p.split ? ld_cluster4(saddr(part + c * PAD_N + 4 * lane), r) : make_float4(0.f, 0.f, 0.f, 0.f);
         float4 sum = v[0];
 #pragma unroll
         for (int r = 1; r < MAX_SPLIT; ++r)
           if (r < p.split) {
             sum.x += v[r].x; sum.y += v[r].y; sum.z += v[r].z; sum.w += v[r].w;
           }
-        const int64_t off = (int64_t)c * p.ld_out + n_first + o;
-        const float e[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n_first + o + i < n_end) store_out(p, off + i, e[i]);
+        store4(p, c, first, 4 * lane, sum);
       }
     }
     cluster_sync();                // no CTA leaves while another reads its shared memory
@@ -464,9 +451,9 @@ void choose_tiles(int64_t N, int cols, int kbs, int* bn, int* split) {
 
 }  // namespace gtc
 
-// Calls with more rows of a than this take the pairs of CTAs: 64 x 154880 x 6144 takes 153 us here and 190 there, 64 x
-// 6144 x 12288 24.5 and 27.0.  With tiles of 128 columns (32 per epilogue warp) this kernel took 196 us for 80 x 154880 x
-// 6144 and 209 for 128, the pairs 192 and 198; 128 x 2048 x 6144 11.5 against 13.3.
+// Calls with more rows of a than this take the pairs of CTAs: 64 x 154880 x 6144 takes 150 us here and 190 there, 64 x
+// 6144 x 12288 19.7 and 27.0.  With tiles of 128 columns an earlier form of this kernel took 196 us for 80 x 154880 x 6144
+// and 209 for 128 rows, the pairs 192 and 198; 128 x 2048 x 6144 11.5 against 13.3.
 constexpr int64_t kPairRows = 64;
 static_assert(kPairRows == gtc::COLS, "a tile holds every row of a");
 
@@ -500,6 +487,8 @@ int launch_gemm_fp8(const GemmFp8Plan& g, cudaStream_t st) {
   }
   p.tiles = (int)tiles;
   p.out_f32 = g.out_f32;
+  p.sets = p.cols <= 32 ? 4 : 2;
+  p.vec_out = g.ld_out % 4 == 0 && (uintptr_t)g.out % (g.out_f32 ? 16 : 8) == 0;
   p.vec_scales = p.kbs % 4 == 0 && (uintptr_t)g.a_scale % 16 == 0 && (uintptr_t)g.w_scale % 16 == 0;
   p.status = g.status;
   CUtensorMap mw, ma;
