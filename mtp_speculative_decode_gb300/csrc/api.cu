@@ -4,7 +4,7 @@
 #include <stdio.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "head.h"
 
 namespace mtpsd {
 

@@ -6,7 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "head.h"
 #include "mbar.cuh"
 
 namespace mtpsd {

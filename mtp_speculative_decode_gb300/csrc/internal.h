@@ -5,8 +5,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "../../include/mtpsd.h"
-
 namespace mtpsd {
 
 // Block-table indirection of a paged cache (bt == nullptr: contiguous, pool row cache_start[b] + s).
@@ -47,26 +45,6 @@ int launch_accept_stochastic(const int64_t* draft, const float* q, const float* 
 int launch_bounded_wait_check(int64_t limit_ns, int32_t* status, int64_t* out, cudaStream_t st);
 int launch_share_gather(const int32_t* s0, const uint32_t* ro, const int32_t* n_acc, int B, int k,
                         int32_t* out, const int64_t* row_pos, int64_t* shared_pos, int32_t* status, cudaStream_t st);
-
-// FP8 product with block-128 scales
-struct GemmFp8Plan {
-  const uint8_t* a; const float* a_scale;
-  const uint8_t* w; const float* w_scale; int w_scale_rows;
-  int64_t M, N, K;
-  bool out_f32; void* out; int64_t ld_out;
-  int32_t* status;
-};
-int launch_gemm_fp8(const GemmFp8Plan& p, cudaStream_t st);
-int launch_gemm_fp8_pair(const GemmFp8Plan& p, cudaStream_t st);   // many rows: pairs of CTAs (K > 0)
-
-// logits of the verify rows and the token table of their penalties
-int launch_process_logits(const mtpsd_logits_args& a, cudaStream_t st);
-int launch_token_counts_build(const int64_t* tokens, int64_t S, const uint32_t* offsets, const int64_t* n_prompt, int B,
-                              int64_t V, int16_t* counts, int64_t ld, int n_rows, const int32_t* rows, int32_t* status,
-                              cudaStream_t st);
-int launch_token_counts_accept(const int64_t* draft, const int32_t* n_acc, const int64_t* next, int B, int K, int64_t V,
-                               int16_t* counts, int64_t ld, int n_rows, const int32_t* rows, int32_t* status,
-                               cudaStream_t st);
 
 // indexer scores into a [R, ld] float matrix (positions > row_pos are not written)
 struct IndexerPlan {

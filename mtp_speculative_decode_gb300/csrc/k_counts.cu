@@ -13,7 +13,7 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "internal.h"
+#include "head.h"
 
 namespace mtpsd {
 

@@ -31,7 +31,7 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "internal.h"
+#include "head.h"
 #include "mbar.cuh"
 
 namespace mtpsd {
