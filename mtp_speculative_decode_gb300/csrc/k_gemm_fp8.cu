@@ -451,9 +451,9 @@ void choose_tiles(int64_t N, int cols, int kbs, int* bn, int* split) {
 
 }  // namespace gtc
 
-// Calls with more rows of a than this take the pairs of CTAs: 64 x 154880 x 6144 takes 150 us here and 190 there, 64 x
-// 6144 x 12288 19.7 and 27.0.  With tiles of 128 columns an earlier form of this kernel took 196 us for 80 x 154880 x 6144
-// and 209 for 128 rows, the pairs 192 and 198; 128 x 2048 x 6144 11.5 against 13.3.
+// Calls with more rows of a than this take the pairs of CTAs: 64 x 154880 x 6144 takes 150 us here and 185 there, 64 x
+// 6144 x 12288 19.7 and 27. With tiles of 128 columns an earlier form of this kernel took 196 us for 80 x 154880 x 6144
+// and 209 for 128 rows, the pairs 185 and 192; 128 x 2048 x 6144 11.5 against 13.3.
 constexpr int64_t kPairRows = 64;
 static_assert(kPairRows == gtc::COLS, "a tile holds every row of a");
 

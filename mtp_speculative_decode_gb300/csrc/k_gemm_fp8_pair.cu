@@ -20,11 +20,12 @@
 //   warp 8      TMA producer of this CTA's operands; both CTAs' copies complete on the leader's barrier.
 //   warp 9      TMEM allocation; in the leader (even) CTA the MMA issue for the pair.
 //   warp 10     scales of this CTA's rows of a;  warp 11  scales of the tile's weight rows.
-// What bounds it: 768 x 154880 x 6144 takes 586 us, 2.5 PFLOP/s: the tensor cores are busy half of the time, and an epilogue
-// warp's 950 cycles a block (eight reads of TMEM of 45, the fetch of the next scales and barrier 180, the hand-over of
-// the buffer and the first read's latency most of the rest) set the pace.  Handing the buffer over in two halves, so that
-// four are in flight, doubled the hand-overs and took 727 us; reads of 32 columns spilled (681 us).  Back to back on random
-// codes the GPU draws 1385 of its 1400 W (zeros: 755 W at the same speed), so that a shorter chain would give little.
+// What bounds it: 768 x 154880 x 6144 takes 564 us, 2.6 PFLOP/s: the tensor cores are busy half of the time, and an epilogue
+// warp's 910 cycles a block set the pace (the reads of TMEM and the additions 400, the fetch of the next scales and barrier
+// 180, the hand-over of the buffer and the first read's latency most of the rest).  Reads of 16 columns at a time took 583
+// us; handing the buffer over in two halves, so that four are in flight, doubled the hand-overs (727 us); the next block's
+// first read in front of this block's last additions spilled (667 us).  Back to back on random codes the GPU draws 1385 of
+// its 1400 W (zeros: 755 W at the same speed), so that a shorter chain would give little.
 // With few tiles the blocks of K are split over up to 4 pairs of one cluster.
 #include <algorithm>
 
@@ -371,43 +372,50 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
         tc_fence_after();
         const uint32_t taddr = taddr0 + (uint32_t)(buf * COLS);
         if (live) {
-          // 16 columns x 32 lanes at a time; the next read is in flight while one is added
-          uint32_t t[2][16];
-          auto read = [&](int c) {
+          // the 32 columns of a run x 32 lanes at a time; the next run's read is in flight while one is added
+          uint32_t t[2][32];
+          auto read = [&](int r) {
             if constexpr (ROWS1) {
-              tmem_ld_x2(taddr + 64 * (c / PW) + 16 * (c % PW), t[c & 1]);
-              tmem_ld_x2(taddr + (16u << 16) + 64 * (c / PW) + 16 * (c % PW), t[c & 1] + 8);
+              tmem_ld_x2(taddr + 64 * r, t[r & 1]);
+              tmem_ld_x2(taddr + (16u << 16) + 64 * r, t[r & 1] + 8);
+              tmem_ld_x2(taddr + 64 * r + 16, t[r & 1] + 16);
+              tmem_ld_x2(taddr + (16u << 16) + 64 * r + 16, t[r & 1] + 24);
             } else {
-              tmem_ld_rows16(taddr + 64 * (c / PW) + 16 * (c % PW), t[c & 1]);
+              tmem_ld_rows16(taddr + 64 * r, t[r & 1]);
+              tmem_ld_rows16(taddr + 64 * r + 16, t[r & 1] + 16);
             }
           };
           read(0);
 #pragma unroll
-          for (int c = 0; c < NP * PW; ++c) {
+          for (int r = 0; r < NP; ++r) {
             tmem_ld_wait();
-            if (c + 1 < NP * PW) {
-              read(c + 1);
+            if (r + 1 < NP) {
+              read(r + 1);
             } else {               // the warp's last read of the buffer
               tc_fence_before();
               __syncwarp();
               if (lane == 0) arrive_at(te0 + 8 * buf);
               if constexpr (!ROWS1) fetch_next();
             }
-            if constexpr (ROWS1) {
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const uint64_t s = *(const uint64_t*)(scw + 64 * (c / PW) + 16 * (c % PW) + c0 + 8 * g + fc);
+            for (int h = 0; h < 2; ++h) {
+              const int c = 2 * r + h;
+              const uint32_t* tt = t[r & 1] + 16 * h;
+              if constexpr (ROWS1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint64_t& q = acc[8 * c + 4 * g + i];
-                  const uint32_t* v = t[c & 1] + 8 * (i >> 1) + 4 * g + 2 * (i & 1);
-                  q = fma2(pack2(v[0], v[1]), mul2(s, pack2(make_float2(rs[i], rs[i]))), q);
+                for (int g = 0; g < 2; ++g) {
+                  const uint64_t s = *(const uint64_t*)(scw + 64 * r + 16 * h + c0 + 8 * g + fc);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    uint64_t& q = acc[8 * c + 4 * g + i];
+                    const uint32_t* v = tt + 8 * (i >> 1) + 4 * g + 2 * (i & 1);
+                    q = fma2(pack2(v[0], v[1]), mul2(s, pack2(make_float2(rs[i], rs[i]))), q);
+                  }
                 }
-              }
-            } else {
+              } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                acc[8 * c + i] = fma2(pack2(t[c & 1][2 * i], t[c & 1][2 * i + 1]), ws[c / PW], acc[8 * c + i]);
+                for (int i = 0; i < 8; ++i) acc[8 * c + i] = fma2(pack2(tt[2 * i], tt[2 * i + 1]), ws[r], acc[8 * c + i]);
+              }
             }
           }
           if constexpr (ROWS1) fetch_next();
