@@ -92,6 +92,18 @@ def test_product(mt, M, N, K, out, w_rows):
     check_product(got, a, sa, w, sw, w_rows)
 
 
+@pytest.mark.parametrize("w_rows", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 40000, 384), (16, 40001, 640), (20, 60011, 128), (32, 30000, 1408), (33, 40007, 640),
+                                   (64, 60000, 1152), (65, 50001, 384), (200, 40000, 640), (300, 30001, 896)])
+def test_product_many_tiles_per_cta(mt, M, N, K, w_rows):
+    """Several tiles a CTA, with numbers of blocks that are no multiple of the rings, slots, buffers and sets."""
+    a, sa, w, sw = product_case(M + N, M, N, K, w_rows)
+    st = status()
+    got = mt.gemm_fp8_block128(dev(a), dev(sa), dev(w), dev(sw), dev_status=st)
+    assert st.item() == 0
+    check_product(got, a, sa, w, sw, w_rows)
+
+
 @pytest.mark.parametrize("M,N,K", [(0, 128, 256), (4, 0, 256), (5, 130, 0), (0, 0, 0)])
 def test_product_empty(mt, M, N, K):
     a, sa, w, sw = product_case(0, M, N, K, 1)
@@ -424,6 +436,27 @@ def test_logits(mt, B, K, V, parts, dtype):
     masked_out = any(c.oracle(r)[1] < 0 for r in range(c.R)) if V < 2000 else False
     if V < 2000:
         assert st.item() == (16 if masked_out else 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,K,V", [(400, 5, 701), (150, 5, 20000), (90, 7, 40003)])
+def test_logits_many_rows_per_cluster(mt, B, K, V, dtype):
+    """More rows than run at once, ragged requests (empty ones too): rows of one and of several requests in a run."""
+    rng = np.random.default_rng(B + V)
+    n = rng.integers(0, K + 3, B)
+    n[1] = 0
+    c = Case(B, B, K, V, dtype, rows_per=n, **{**ALL, "bias": 40})
+    probs, out = torch.full((c.R, V), 9.0, device="cuda"), torch.full((c.R, V), 9.0, device="cuda")
+    argmax = c.call(mt, argmax=torch.empty(c.R, dtype=torch.int64, device="cuda"), probs=probs, out_logits=out)
+    rows = rng.permutation(c.R)[:150]
+    c.check(argmax, probs, out, rows)
+    again = torch.empty_like(out)
+    assert torch.equal(c.call(mt), argmax)             # the greedy token alone
+    c.call(mt, out_logits=again)
+    assert torch.equal(again.nan_to_num(nan=1.5), out.nan_to_num(nan=1.5))
+    other = torch.empty_like(probs)
+    c.call(mt, probs=other)
+    assert torch.equal(other, probs)
 
 
 @pytest.mark.parametrize("V", [262144, 393216])
