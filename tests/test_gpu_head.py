@@ -629,6 +629,72 @@ def test_logits_bad_device_values(mt):
     c.check(None, None, out)
 
 
+def test_logits_offsets_past_the_rows(mt):
+    """Offsets that pass the rows of the arrays are cut to them and flagged; offsets that fall stay inside them."""
+    from mtp_speculative_decode_gb300 import _native as N
+    c = Case(17, 4, 2, 300, torch.float32, counts=True, pen=True, bias=5)
+    want = torch.empty(c.R, 300, device="cuda")
+    c.call(mt, out_logits=want)
+    off = c.off.copy()
+    off[-1] += 7
+    st, out = status(), torch.full((c.R + 2, 300), 9.0, device="cuda")
+    args = dict(draft=dev(c.draft), counts=dev(c.counts), repetition=dev(c.rep), frequency=dev(c.freq), presence=dev(c.pres),
+                bias_offsets=u32(c.bias[0]), bias_tokens=dev(c.bias[1]), bias_values=dev(c.bias[2]))
+    mt.process_logits(c.logits.cuda(), u32(off), out_logits=out[:c.R], dev_status=st, **args)
+    assert st.item() == N.STATUS_ROW_RANGE and torch.equal(out[:c.R], want) and (out[c.R:] == 9).all()
+    off[:] = [0, 9, 3, 6, 12]
+    out.fill_(9.0)
+    mt.process_logits(c.logits.cuda(), u32(off), out_logits=out[:c.R], dev_status=status(), **args)
+    assert (out[c.R:] == 9).all()
+
+
+def test_logits_and_table_on_two_streams_and_in_two_graphs(mt):
+    V = 30011
+    cases = [Case(90 + i, 20, 3, V, (torch.float32, torch.bfloat16)[i], **{**ALL, "bias": 20}) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    off, tokens = u32(np.arange(0, 2001, 100)), dev(np.random.default_rng(3).integers(0, V, 2000).astype(np.int64))
+    ld = mt.token_counts_ld(V)
+    tables = [torch.zeros(20, ld, dtype=torch.int16, device="cuda") for _ in range(2)]
+    argmax = [torch.zeros(c.R, dtype=torch.int64, device="cuda") for c in cases]
+    probs = [torch.zeros(c.R, V, device="cuda") for c in cases]
+    inputs = []
+    for c in cases:
+        a = dict(draft=dev(c.draft), repetition=dev(c.rep), frequency=dev(c.freq), presence=dev(c.pres),
+                 temperature=dev(c.temp), bias_offsets=u32(c.bias[0]), bias_tokens=dev(c.bias[1]),
+                 bias_values=dev(c.bias[2]), bitmask=dev(c.mask), mask_rows=dev(c.mask_rows))
+        inputs.append((c.logits.cuda(), u32(c.off), a))
+        c.counts = ologits.token_counts_build(np.zeros((20, ld), np.int16), tokens.cpu().numpy(), off.cpu().numpy(), V)
+    torch.cuda.synchronize()
+
+    def step(i, stream=None):
+        mt.token_counts_build(tokens, off, V, counts=tables[i], stream=stream)
+        x, o, a = inputs[i]
+        mt.process_logits(x, o, counts=tables[i], argmax=argmax[i], probs=probs[i], stream=stream, **a)
+
+    def check():
+        torch.cuda.synchronize()
+        for i, c in enumerate(cases):
+            c.check(argmax[i], probs[i], rows=range(0, c.R, 9))
+            tables[i].zero_(), argmax[i].zero_(), probs[i].zero_()
+        torch.cuda.synchronize()
+
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            step(i, s)
+    check()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            step(i)
+    assert not any(t.any() for t in tables)            # captured, not run
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    check()
+
+
 def test_logits_mask_by_row_and_empty_batch(mt):
     V = 70
     c = Case(8, 2, 1, V)
