@@ -581,7 +581,7 @@ int resident_clusters(int split) {
 }
 
 // The tile width (64 np) and the pairs per tile (a split of K) with the shortest modelled time: waves of tiles, each of
-// its blocks (cycles per block measured at 256 outputs: 940, of which about 200 do not depend on the width) and a fixed cost
+// its blocks (940 cycles a block at 256 outputs, where 910 were measured; about 200 do not depend on the width) and a fixed cost
 // (start of the pipeline, store; with a split the join through distributed shared memory).
 void choose_tiles(int64_t N, int n_mt, int kbs, int* np, int* split) {
   const double fixed = 5000, join = 5000;
