@@ -1,7 +1,8 @@
 """Python binding of libmtpsd: the C-ABI calls under the same names, taking
 torch CUDA tensors.  Argument marshalling only: every step runs in the
-library's CUDA kernels on the current torch stream (or the stream given).
-Outputs not passed in are allocated with torch before the call."""
+library's CUDA kernels on the current torch stream (or the stream given: a
+torch stream or a raw handle).  Outputs not passed in are allocated with torch
+before the call, in the memory of the stream that the call runs on."""
 from __future__ import annotations
 
 import ctypes as C
@@ -35,6 +36,20 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: Optional[int] = None):
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+
+
+def _empty(stream, *shape, dtype, device) -> torch.Tensor:
+    """A new output.  torch's allocator hands a freed block out again in the order of the stream it was allocated on, so
+    with a stream given the block has to be that stream's: one of the current stream may still be in use there, and after
+    the caller has dropped it the current stream could take it while the call still writes."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream).value or 0
+        # 0 and 1 are the handles of the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 class Workspace:
@@ -87,9 +102,9 @@ def merge_tokens(prompt_tokens, prompt_offsets, draft_tokens, merged_tokens=None
     if prompt_offsets.numel() != B + 1:
         raise ValueError("prompt_offsets must have B+1 entries")
     if merged_tokens is None:
-        merged_tokens = torch.empty(S + B * K, dtype=torch.int64, device=prompt_tokens.device)
+        merged_tokens = _empty(stream, S + B * K, dtype=torch.int64, device=prompt_tokens.device)
     if merged_offsets is None:
-        merged_offsets = torch.empty(B + 1, dtype=torch.uint32, device=prompt_tokens.device)
+        merged_offsets = _empty(stream, B + 1, dtype=torch.uint32, device=prompt_tokens.device)
     check("mtpsd_merge_tokens", lib().mtpsd_merge_tokens(
         _ptr(prompt_tokens), S, _ptr(prompt_offsets), _ptr(draft_tokens), B, K,
         _ptr(merged_tokens), _ptr(merged_offsets), _stream(stream)))
@@ -112,7 +127,7 @@ def pack_latent_fp8(latent, packed=None, stream=None):
         raise ValueError("latent rows must have 576 values")
     T = latent.shape[0]
     if packed is None:
-        packed = torch.empty(T, 656, dtype=torch.uint8, device=latent.device)
+        packed = _empty(stream, T, 656, dtype=torch.uint8, device=latent.device)
     check("mtpsd_pack_latent_fp8", lib().mtpsd_pack_latent_fp8(
         _ptr(latent), N.MTPSD_F32 if f32 else N.MTPSD_BF16, T, _ptr(packed), _stream(stream)))
     return packed
@@ -141,9 +156,9 @@ def quantize_fp8_block128(x, codes=None, scales=None, stream=None):
         raise ValueError("x must hold a multiple of 128 values")
     nb = x.numel() // 128
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = _empty(stream, x.shape, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(x.shape[:-1] + (x.shape[-1] // 128,), dtype=torch.float32, device=x.device)
+        scales = _empty(stream, x.shape[:-1] + (x.shape[-1] // 128,), dtype=torch.float32, device=x.device)
     check("mtpsd_quantize_fp8_block128", lib().mtpsd_quantize_fp8_block128(
         _ptr(x), nb, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
@@ -212,7 +227,7 @@ def indexer_topk(q, q_scale, weights, k_cache, k_scale, cache_start, row_offsets
     R = q.shape[0]
     B = row_offsets.numel() - 1
     if topk_idx is None:
-        topk_idx = torch.empty(R, topk, dtype=torch.int32, device=q.device)
+        topk_idx = _empty(stream, R, topk, dtype=torch.int32, device=q.device)
     nbytes = indexer_topk_aux_bytes(B, R, max_visible, topk) if scores is not None else \
         indexer_topk_workspace_size(B, R, max_visible, topk)
     ws = _ws(workspace, nbytes, q.device)
@@ -232,7 +247,7 @@ def indexer_scores(q, q_scale, weights, k_cache, k_scale, cache_start, row_offse
     R = q.shape[0]
     B = row_offsets.numel() - 1
     if scores is None:
-        scores = torch.empty(R, scores_ld(max_visible), dtype=torch.float32, device=q.device)
+        scores = _empty(stream, R, scores_ld(max_visible), dtype=torch.float32, device=q.device)
     ws = _ws(workspace, indexer_plan_bytes(B, R), q.device)
     a = _indexer_args(q, q_scale, weights, k_cache, k_scale, cache_start, row_offsets, row_pos, 1, max_visible,
                       None, None, scores, ws, dev_status)
@@ -251,7 +266,7 @@ def topk(scores, row_len, max_len: int, k: int, out_idx=None, out_score=None, de
     _need(row_len, "row_len", torch.int64, 1)
     R, ld = scores.shape
     if out_idx is None:
-        out_idx = torch.empty(R, k, dtype=torch.int32, device=scores.device)
+        out_idx = _empty(stream, R, k, dtype=torch.int32, device=scores.device)
     nbytes = topk_workspace_size(R, max_len, k)
     ws = _ws(workspace, nbytes, scores.device) if nbytes else None
     check("mtpsd_topk", lib().mtpsd_topk(
@@ -310,7 +325,7 @@ def sparse_mla_decode(q, latent, cache_start, row_offsets, row_pos, idx, softmax
     R, H, DL = q.shape
     dt = N.MTPSD_FP8_DS_MLA if fp8kv else (N.MTPSD_BF16 if bf16 else N.MTPSD_F32)
     if out is None:
-        out = torch.empty(R, H, 512, dtype=q.dtype, device=q.device)
+        out = _empty(stream, R, H, 512, dtype=q.dtype, device=q.device)
     nbytes = sparse_mla_workspace_size(R, H, idx.shape[1], n_append, dt)
     ws = _ws(workspace, nbytes, q.device) if nbytes else workspace
     a = N.MlaArgs(B=row_offsets.numel() - 1, R=R, n_heads=H, d_latent=DL, d_v=512, n_idx=idx.shape[1],
@@ -341,9 +356,9 @@ def accept_greedy(draft, target_argmax, magic_draft_id: int = -1, num_accepted=N
     if target_argmax.shape != (B, K + 1):
         raise ValueError("target_argmax must be [B, K+1]")
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=torch.int32, device=draft.device)
+        num_accepted = _empty(stream, B, dtype=torch.int32, device=draft.device)
     if next_tokens is None:
-        next_tokens = torch.empty(B, dtype=torch.int64, device=draft.device)
+        next_tokens = _empty(stream, B, dtype=torch.int64, device=draft.device)
     check("mtpsd_accept_greedy", lib().mtpsd_accept_greedy(
         _ptr(draft), _ptr(target_argmax), B, K, magic_draft_id, _ptr(num_accepted), _ptr(next_tokens),
         _stream(stream)))
@@ -366,9 +381,9 @@ def accept_stochastic(draft, draft_probs, target_probs, u_accept, u_sample, num_
         raise ValueError("shapes must be draft [B,K], draft_probs [B,K,V], target_probs [B,K+1,V], "
                          "u_accept [B,K], u_sample [B]")
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=torch.int32, device=draft.device)
+        num_accepted = _empty(stream, B, dtype=torch.int32, device=draft.device)
     if next_tokens is None:
-        next_tokens = torch.empty(B, dtype=torch.int64, device=draft.device)
+        next_tokens = _empty(stream, B, dtype=torch.int64, device=draft.device)
     check("mtpsd_accept_stochastic", lib().mtpsd_accept_stochastic(
         _ptr(draft), _ptr(draft_probs), _ptr(target_probs), _ptr(u_accept), _ptr(u_sample), B, K, V,
         _ptr(num_accepted), _ptr(next_tokens), _ptr(dev_status), _stream(stream)))
@@ -412,11 +427,11 @@ def topk_share_gather(step0_topk, row_offsets, num_accepted=None, shared_idx=Non
     B = row_offsets.numel() - 1
     k = step0_topk.shape[1]
     if shared_idx is None:
-        shared_idx = torch.empty(B, k, dtype=torch.int32, device=step0_topk.device)
+        shared_idx = _empty(stream, B, k, dtype=torch.int32, device=step0_topk.device)
     if row_pos is not None:
         _need(row_pos, "row_pos", torch.int64, 1)
         if shared_pos is None:
-            shared_pos = torch.empty(B, dtype=torch.int64, device=step0_topk.device)
+            shared_pos = _empty(stream, B, dtype=torch.int64, device=step0_topk.device)
     check("mtpsd_topk_share_gather", lib().mtpsd_topk_share_gather(
         _ptr(step0_topk), _ptr(row_offsets), _ptr(num_accepted), B, k, _ptr(shared_idx), _ptr(row_pos),
         _ptr(shared_pos if row_pos is not None else None), _ptr(dev_status), _stream(stream)))
@@ -437,7 +452,7 @@ def assign_cache_locs(block_table, page_size: int, start_pos, W: int, out_cache_
     _need(start_pos, "start_pos", torch.int64, 1)
     B = start_pos.numel()
     if out_cache_loc is None:
-        out_cache_loc = torch.empty(B, W, dtype=torch.int64, device=start_pos.device)
+        out_cache_loc = _empty(stream, B, W, dtype=torch.int64, device=start_pos.device)
     pk = _paged((block_table, page_size))
     check("mtpsd_assign_cache_locs", lib().mtpsd_assign_cache_locs(
         C.byref(pk), B, _ptr(start_pos), W, _ptr(out_cache_loc), _ptr(dev_status), _stream(stream)))
@@ -574,7 +589,7 @@ def gemm_fp8_block128(a, a_scale, w, w_scale, out=None, out_dtype=None, dev_stat
     else:
         raise ValueError("w_scale must be [N, K/128] or [ceil(N/128), K/128]")
     if out is None:
-        out = torch.empty(M, n_out, dtype=out_dtype or torch.bfloat16, device=a.device)
+        out = _empty(stream, M, n_out, dtype=out_dtype or torch.bfloat16, device=a.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     po, ld = _rows(out, "out", dev, _OUT_TYPES, M, n_out)
@@ -622,7 +637,7 @@ def token_counts_build(tokens, offsets, V: int, n_prompt=None, counts=None, coun
     if counts is None:
         if count_rows is not None:
             raise ValueError("count_rows needs a table")
-        counts = torch.empty(B, token_counts_ld(V), dtype=torch.int16, device=tokens.device)
+        counts = _empty(stream, B, token_counts_ld(V), dtype=torch.int16, device=tokens.device)
     pc, pr = _counts(counts, V, B, count_rows, dev)
     check("mtpsd_token_counts_build", lib().mtpsd_token_counts_build(
         pt, tokens.numel(), po, pn, B, V, pc, counts.shape[1], counts.shape[0], pr, _status_ptr(dev_status, dev),
@@ -716,7 +731,7 @@ def process_logits(logits, row_offsets, draft=None, counts=None, count_rows=None
         if mask_rows.numel() != R:
             raise ValueError("mask_rows must have one entry per row")
     if argmax is None and probs is None and out_logits is None:
-        argmax = torch.empty(R, dtype=torch.int64, device=logits.device)
+        argmax = _empty(stream, R, dtype=torch.int64, device=logits.device)
     p_arg = None
     if argmax is not None:
         if argmax.numel() != R:
