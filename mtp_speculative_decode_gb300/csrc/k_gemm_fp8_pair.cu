@@ -114,9 +114,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 v) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
   return *(const uint32_t*)&b;
 }
-__device__ __forceinline__ bool wait_all_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar::wait<true>(bar, parity, abort_flag, status, mbar::DEFAULT_LIMIT_NS));
-}
 
 // NP: a tile has 64 NP outputs.  ROWS1: the weight's scales are per row and block (else per 128 x 128 block).
 template <int NP, bool ROWS1>
@@ -198,6 +195,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
           if (++stage == NSTAGE) stage = 0;
         }
       }
+      // The leader's commits arrive in both CTAs: every one is awaited, so that none is still on its way to the shared
+      // memory of a CTA that has left.
+      for (int s = 0; s < NSTAGE && ok; ++s) {
+        const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);     // loads of stage s
+        if (issued > 0) ok = wait_all(&empty[s], (issued - 1) & 1, abort_flag, p.status);
+      }
       if (*abort_flag && side == 0 && lane == 0) {   // drain the pair's copies still in flight (bounded)
         volatile int dummy = 0;
         for (int s = 0; s < NSTAGE; ++s) {
@@ -205,8 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
           if (issued > 0) mbar::wait<true>(&full[s], (issued - 1) & 1, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
         }
       }
-    } else if (warp == MMA_WARP && side == 0) {
-      if (elect_one()) {           // one thread waits and issues
+    } else if (warp == MMA_WARP) {
+      if (side == 0 && elect_one()) {      // one thread of the pair waits and issues
         int stage = 0, n = 0;
         bool ok = true;
         const uint32_t id = (1u << 4) | ((uint32_t)BN >> 3 << 17) | ((256u >> 4) << 24);   // M = 256, N = BN
@@ -232,8 +235,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
         mma_commit_pair(drain, mask);                    // every MMA has completed before TMEM is released
       }
       __syncwarp();
-      volatile int dummy = 0;
-      mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
+      volatile int dummy = 0;              // in both CTAs: the last commit arrives in both
+      mbar::wait<true>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
     } else if (warp >= SCALE_WARP) {
       // slot: [SG][128] scales of this CTA's rows of a, then [SG][256] of the tile's weight rows (ROWS1) or
       // [SG][4] of the blocks of its runs of 64
