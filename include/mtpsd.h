@@ -515,6 +515,8 @@ int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted,
  * n_bias MTPSD_STATUS_INDEX_RANGE; count_rows (as the token table; -1: nothing counted) and mask_rows (-1: no mask)
  * outside their arrays and a row_offsets[B] past R (cut to it) MTPSD_STATUS_ROW_RANGE.  V <= 393216,
  * K + n_bias < 2^31.  Apart from out_logits = logits no output may overlap an input.
+ * Where a wait expires (MTPSD_STATUS_WAIT_TIMEOUT), rows that were not finished are left as they were; only out_logits may
+ * hold a part of one.
  */
 typedef struct {
   int32_t B;                   /* requests */

@@ -26,13 +26,15 @@
 // All values, the maximum and the sums are float32; the sums add at most chunk /
 // 256 values per thread before the tree, in an order fixed by the sizes.  The
 // exponentials are 2^y, y = (x - m_c) (log2 e / T): y is off by less than 2^-22.5 of its value.
+// Every mbarrier wait is bounded (2 s): on expiry the kernel flags MTPSD_STATUS_WAIT_TIMEOUT, the cluster leaves its rows
+// from there on, and each CTA waits for its copies in flight before it returns.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "head.h"
-#include "mbar.cuh"
+#include "head_wait.cuh"
 
 namespace mtpsd {
 namespace lgt {
@@ -134,7 +136,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
   __shared__ Request R;
   __shared__ float s_red[WARPS];
   __shared__ unsigned s_idx;
-  __shared__ int s_rep[REPEATS], s_reps, s_list, s_abort;
+  __shared__ int s_rep[REPEATS], s_reps, s_list;
+  __shared__ int s_abort, s_told;                          // a wait of this CTA has expired; the CTA leaves
   __shared__ __align__(16) float4 s_peer[2][MAX_CLUSTER];   // (maximum, sum, position) of every CTA, by the row's parity
   __shared__ float4 s_row;                                  // the row's (maximum, sum, position)
   __shared__ __align__(8) uint64_t s_bar[2], s_in;
@@ -157,6 +160,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
   const int bulk = p.vec_in ? len * ES & ~15 : 0;
   if (tid == 0) {
     s_abort = 0;
+    s_told = 0;
     for (int i = 0; i < 2; ++i) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&s_bar[i])));
       expect_tx(&s_bar[i], p.cluster * 16);
@@ -377,14 +381,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
         atomicOr(&skip[c >> 5], 1u << (c & 31));
       }
     }
-    // the thread's largest value: of the step's group at bg (-1: none yet), or of a single token si
+    // the thread's largest value: of the step's group at bg (-1: none yet), or of a single token (si: its position + 1, as
+    // in s_idx: 0 is an expired wait)
     float best = -INFINITY, sbest = -INFINITY;
     int bg = -1;
     unsigned si = 0xffffffffu;
     auto open = [&](int c) { return !rm || bit(mask, c); };
     auto single = [&](int c, float x) {                // a token computed on its own
       if (!open(c)) x = -INFINITY;
-      const unsigned t = (unsigned)(start + c);
+      const unsigned t = (unsigned)(start + c) + 1;
       if (keep) xs[c] = x;
       if (out) out[c] = x;
       // NaN above everything, then the larger value, then the lower position
@@ -397,9 +402,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
 
     // ---- the chunk
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (warp == 0) mbar::wait<false>(&s_in, in_phase, &s_abort, a.dev_status, mbar::DEFAULT_LIMIT_NS);
+    if (warp == 0 && !mbar::wait_head<false>(&s_in, in_phase, &s_abort, a.dev_status)) {
+      mbar::drain<false>(&s_in, in_phase, a.dev_status);     // nothing of the copy is in flight when the CTA leaves
+      if (p.cluster == 1) s_told = 1;
+    }
     in_phase ^= 1;
     __syncthreads();                                   // the chunk is staged, the marks are set
+    // When a wait of a CTA has expired, here or in the exchange of the row before, the CTA goes through the row with what is
+    // there but stores nothing, and the exchange tells the cluster: none of its CTAs stores the row's argmax and
+    // probabilities, and all leave here in the next row, with no copy of theirs and no peer's values in flight.  (Leaving
+    // behind the exchange took 107.7 us for 768 rows of 154880, argmax only, where 106.0 are reached and 105.8 without any
+    // of this.)
+    if (__builtin_expect(s_told, 0)) return;
+    if (out && s_abort) out = nullptr;
 #pragma unroll 2
     for (int s = 0; s < steps; ++s) {
       const int c = (s * THREADS + tid) * G;
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
           eq |= (uint32_t)(nan ? x != x : x == m) << e;
         }
         eq &= ~(uint32_t)((const uint8_t*)skip)[bg >> 3] & (rm ? (uint32_t)((const uint8_t*)mask)[bg >> 3] : ALL);
-        if (eq) idx = min(idx, (unsigned)(start + bg + __ffs(eq) - 1));
+        if (eq) idx = min(idx, (unsigned)(start + bg + __ffs(eq)));
       }
       if (idx != 0xffffffffu) atomicMin(&s_idx, idx);
     }
@@ -612,13 +627,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
     unsigned arg = s_idx;
     if (p.cluster > 1) {
       if (warp == 0) {           // one warp exchanges and waits; the others sleep at the block's barrier
+        if (s_abort) {           // a NaN passes every other maximum, a position of 0 every other NaN
+          m = NAN;
+          arg = 0;
+        }
         if (lane < p.cluster)
           asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
                            map_rank(&s_peer[parity][rank], lane)),
                        "r"(__float_as_uint(m)), "r"(__float_as_uint(sum)), "r"(arg), "r"(0u), "r"(map_rank(&s_bar[parity], lane))
                        : "memory");
         __syncwarp();
-        mbar::wait<true>(&s_bar[parity], bar_phase, &s_abort, a.dev_status, mbar::DEFAULT_LIMIT_NS);
+        // where the wait expires, the peers' values may still come: they are not to find a CTA that has left
+        const bool here = mbar::wait_head<true>(&s_bar[parity], bar_phase, &s_abort, a.dev_status) ||
+                          mbar::drain<true>(&s_bar[parity], bar_phase, a.dev_status);
         __syncwarp();
         // armed for the row after the next before this CTA's next values let a peer get there
         if (lane == 0) expect_tx(&s_bar[parity], p.cluster * 16);
@@ -629,6 +650,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
           cm = v.x;
           cs = v.y;
           ci = __float_as_uint(v.z);
+        }
+        if (!here) {
+          cm = NAN;
+          ci = 0;
         }
         float t = cm;
 #pragma unroll
@@ -642,6 +667,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
           cs += __shfl_xor_sync(0xffffffffu, cs, o);
         }
         if (lane == 0) s_row = make_float4(t, cs, __uint_as_float(ci), 0.f);
+        if (lane == 0 && ci == 0) s_told = 1;
       }
       __syncthreads();
       top = s_row.x;
@@ -651,12 +677,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
       parity ^= 1;
     }
     const bool empty = top == -INFINITY;
-    if (rank == 0 && tid == 0) {
-      if (a.argmax) a.argmax[r] = empty ? -1 : (int64_t)arg;
+    if (rank == 0 && tid == 0 && arg != 0) {
+      if (a.argmax) a.argmax[r] = empty ? -1 : (int64_t)arg - 1;
       if (empty) flag_status(a.dev_status, MTPSD_STATUS_EMPTY_ROW);
     }
     // ---- the chunk's probabilities
-    if (a.probs) {
+    if (a.probs && arg != 0) {
       float* o = a.probs + r * a.probs_ld + start;
       const bool stored = keep && !empty;              // else zeros, and one at the greedy token
       // a NaN maximum makes every probability NaN
@@ -666,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
       auto prob = [&](int c) -> float {
         if (bad) return NAN;
         if (stored) return m == -INFINITY ? 0.f : xs[c] * scale;
-        return onehot && !empty && (unsigned)(start + c) == arg ? 1.f : 0.f;
+        return onehot && !empty && (unsigned)(start + c) + 1 == arg ? 1.f : 0.f;
       };
       if (p.vec_probs) {
         const int n4 = len / 4;
