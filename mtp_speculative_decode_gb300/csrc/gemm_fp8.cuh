@@ -7,7 +7,7 @@
 
 #include "common.cuh"
 #include "head.h"
-#include "mbar.cuh"
+#include "head_wait.cuh"
 
 namespace mtpsd {
 namespace gtc {
@@ -29,7 +29,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 // Warp-uniform bounded wait (all 32 lanes): false when it gave up.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar::wait<false>(bar, parity, abort_flag, status, mbar::DEFAULT_LIMIT_NS));
+  return __all_sync(0xffffffffu, mbar::wait_head<false>(bar, parity, abort_flag, status));
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -121,6 +121,12 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t cta_addr, uint32_t rank) 
   float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(cta_addr), "r"(rank));
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster1(uint32_t cta_addr, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(cta_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 }  // namespace gtc

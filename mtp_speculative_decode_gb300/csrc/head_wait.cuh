@@ -32,6 +32,7 @@ __device__ __forceinline__ bool wait_head(uint64_t* bar, uint32_t parity, volati
 // The wait of a kernel that gives up for what is still in flight.
 template <bool CLUSTER>
 __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (try_wait<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!try_wait_sleep<CLUSTER>(bar, parity, SLEEP_HINT_NS))
     if (globaltimer_ns() - t0 > DEFAULT_LIMIT_NS) {

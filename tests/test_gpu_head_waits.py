@@ -55,7 +55,7 @@ def test_products_on_pairs_back_to_back(mt):
             assert torch.equal(o, want[i % len(want)]), (turn, sizes[i % len(want)])
 
 
-ONE_PROBE = ["k_logits.cu"]
+ONE_PROBE = ["k_logits.cu", "k_gemm_fp8.cu"]
 
 
 @pytest.fixture(scope="module")
@@ -132,3 +132,28 @@ def test_logits_after_an_expired_wait(mt, one_probe, monkeypatch, B, K, V, outpu
         assert torch.equal(o[~left], w[~left]) and ((o == w) | (o == MARK)).all()
     again, st = run()                                                # the device works on
     assert st == 0 and all(torch.equal(again[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K,w_rows", [(1, 576, 6144, 1), (64, 640, 12288, 128), (33, 2049, 1920, 1),      # K split over a cluster
+                                          (64, 6144, 12288, 128), (16, 40001, 640, 1), (33, 60000, 256, 128)])
+def test_few_row_product_after_an_expired_wait(mt, one_probe, monkeypatch, M, N, K, w_rows, out):
+    from mtp_speculative_decode_gb300 import _native as nat
+    case = operands(M, N, K, w_rows, seed=N)
+
+    def run():
+        o = torch.full((M, N), -7.0, dtype=out, device="cuda")       # every product is positive
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        mt.gemm_fp8_block128(*case, out=o, dev_status=st)
+        torch.cuda.synchronize()
+        return o, st.item()
+
+    want, st = run()
+    assert st == 0 and (want > 0).all()
+    with monkeypatch.context() as mp:
+        mp.setattr(nat, "_lib", one_probe)
+        got, st = run()
+    left = got == -7
+    assert st == nat.STATUS_WAIT_TIMEOUT and left.any() and torch.equal(got[~left], want[~left])
+    again, st = run()                                                # the device works on
+    assert st == 0 and torch.equal(again, want)
