@@ -102,6 +102,9 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t mask) {
       "h"((uint16_t)mask)
       : "memory");
 }
+__device__ __forceinline__ void st_cluster1(uint32_t cta_addr, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(cta_addr, rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -201,11 +204,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
         const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);     // loads of stage s
         if (issued > 0) ok = wait_all(&empty[s], (issued - 1) & 1, abort_flag, p.status);
       }
-      if (*abort_flag && side == 0 && lane == 0) {   // drain the pair's copies still in flight (bounded)
-        volatile int dummy = 0;
+      // The pair's copies land before its CTAs leave, whoever waits for them: after an expired wait nobody else may.  Copies of
+      // the odd CTA that the leader has not announced have had the limit of that CTA's own waits to land.
+      if (side == 0 && lane == 0) {
         for (int s = 0; s < NSTAGE; ++s) {
           const int issued = n / NSTAGE + (s < n % NSTAGE ? 1 : 0);   // loads of stage s
-          if (issued > 0) mbar::wait<true>(&full[s], (issued - 1) & 1, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
+          if (issued > 0) mbar::drain<true>(&full[s], (issued - 1) & 1, p.status);
         }
       }
     } else if (warp == MMA_WARP) {
@@ -235,8 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
         mma_commit_pair(drain, mask);                    // every MMA has completed before TMEM is released
       }
       __syncwarp();
-      volatile int dummy = 0;              // in both CTAs: the last commit arrives in both
-      mbar::wait<true>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
+      mbar::drain<true>(drain, 0, p.status);        // in both CTAs: the last commit arrives in both
     } else if (warp >= SCALE_WARP) {
       // slot: [SG][128] scales of this CTA's rows of a, then [SG][256] of the tile's weight rows (ROWS1) or
       // [SG][4] of the blocks of its runs of 64
@@ -498,10 +501,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_fp8_pair_kernel(const __grid_
           *(uint64_t*)(ROWS1 ? part + (quarter * 32 + 8 * i + fr) * PART_LD + at + fc
                              : part + (quarter * 32 + lane) * PART_LD + at + 2 * i) = acc[8 * c + 4 * g + i];
         }
+    if (gave_up)                   // these sums are not all there (and copies may still come on top): no CTA is to store the tile
+      for (int q = 0; q < 2 * p.split; ++q) st_cluster1(saddr((const void*)abort_flag), q, 1u);
     cluster_sync();                // (1)
     const int m_first = (first % p.n_mt * 2 + (int)side) * ROWS, n_first = first / p.n_mt * BN;
     const int n_end = min(p.N, n_first + BN);
-    const int rows = min(ROWS, p.M - m_first);              // <= 0: this CTA's rows are past the last
+    const int rows = *abort_flag ? 0 : min(ROWS, p.M - m_first);      // <= 0: this CTA's rows are past the last
     const int r0 = rows > 0 ? part_rank * rows / p.split : 0, r1 = rows > 0 ? (part_rank + 1) * rows / p.split : 0;
     for (int r = r0 + (warp >> 1); r < r1; r += EPI_WARPS / 2) {
       // half a row per warp, four columns per thread, every remote read in flight at once (columns past the
