@@ -1,6 +1,7 @@
 """The head's operators where a launch takes another path than its ordinary one: table builds whose CTAs go through
-several blocks of 32768 tokens, token ids that are no 32-bit numbers inside a run of wide loads, and the verify head with
-grammar masks and bf16 logits.  Tolerances are those of test_gpu_head.py."""
+several blocks of 32768 tokens, token ids that are no 32-bit numbers inside a run of wide loads, prompts, long draft
+chains, arrays past 2^31 elements, and the verify head with grammar masks, bf16 logits and without drafts.  Tolerances are
+those of test_gpu_head.py."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +9,7 @@ import torch
 from oracle import accept as oaccept
 from oracle import fp8 as ofp8
 from oracle import logits as ologits
-from test_gpu_head import ALL, Case, check_product, dev, mt, status, u32  # noqa: F401
+from test_gpu_head import ALL, Case, check_product, dev, mt, product_case, status, u32  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,101 @@ def test_verify_head_under_a_grammar(mt, sampling, dtype):  # noqa: F811
         head.step()
     head.hidden.copy_(dev(rng.normal(size=(R, D)).astype(np.float32)))
     run_and_check(g.replay)
+
+
+@pytest.mark.parametrize("sampling", [False, True])
+def test_verify_head_without_drafts(mt, sampling):  # noqa: F811
+    """K = 0: one row per request, its token and nothing to accept."""
+    from mtp_speculative_decode_gb300.pipeline import VerifyHead
+    rng = np.random.default_rng(41)
+    B, V, D = 7, 1003, 128
+    w, sw = mt.quantize_fp8_block128(dev(rng.normal(size=(V, D)).astype(np.float32)))
+    c = Case(42, B, 0, V, torch.float32, counts=True, pen=True)
+    c.temp = rng.uniform(0.5, 1.5, B).astype(np.float32)
+    params = dict(repetition=dev(c.rep), frequency=dev(c.freq), presence=dev(c.pres), temperature=dev(c.temp))
+    us = rng.random(B).astype(np.float32)
+    extra = dict(draft_probs=torch.empty(B, 0, V, device="cuda"), u_accept=torch.empty(B, 0, device="cuda"),
+                 u_sample=dev(us)) if sampling else {}
+    head = VerifyHead(w, sw, B, 0, counts=dev(c.counts), params=params, logits_dtype=torch.float32, **extra)
+    head.hidden.copy_(dev(rng.normal(size=(B, D)).astype(np.float32)))
+    head.step()
+    torch.cuda.synchronize()
+    c.logits = head.logits.cpu()
+    c.check(head.target_argmax.view(-1), head.target_probs.view(B, V) if sampling else None)
+    n, t = np.zeros(B, np.int32), head.target_argmax.view(-1).cpu().numpy()
+    if sampling:
+        n, t = oaccept.accept_stochastic(np.zeros((B, 0), np.int64), np.zeros((B, 0, V), np.float32),
+                                         head.target_probs.cpu().numpy(), np.zeros((B, 0), np.float32), us)
+    assert head.status.item() == 0 and np.array_equal(head.num_accepted.cpu().numpy(), n)
+    assert np.array_equal(head.next_tokens.cpu().numpy(), t)
+    assert np.array_equal(head.counts.cpu().numpy(), ologits.token_counts_accept(c.counts, V, None, n, t))
+
+
+@pytest.mark.parametrize("w_rows", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(2048, 640, 384), (4099, 300, 256), (20001, 129, 128), (3000, 2049, 640)])
+def test_product_of_a_prompt(mt, M, N, K, w_rows):  # noqa: F811
+    a, sa, w, sw = product_case(M + N, M, N, K, w_rows)
+    st = status()
+    got = mt.gemm_fp8_block128(dev(a), dev(sa), dev(w), dev(sw), dev_status=st)
+    assert st.item() == 0
+    check_product(got, a, sa, w, sw, w_rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K,V", [(700, 3000), (513, 40)])
+def test_logits_long_draft_chains(mt, K, V, dtype):  # noqa: F811
+    """More drafts than fit the entries in shared memory, most of them several times."""
+    c = Case(K, 2, K, V, dtype, **ALL)
+    out = torch.empty(c.R, V, device="cuda")
+    argmax = c.call(mt, argmax=torch.empty(c.R, dtype=torch.int64, device="cuda"), out_logits=out)
+    rows = [0, 1, 2, 300, 511, 512, K - 1, K, K + 1, K + 2, c.R - 2, c.R - 1]
+    c.check(argmax, None, out, rows)
+
+
+def far_rows(R, V, dtype, last):
+    """A view [R, V] whose last row starts `last` elements behind the first."""
+    ld = last // (R - 1) // 64 * 64
+    buf = torch.empty((R - 1) * ld + V, dtype=dtype, device="cuda")
+    return buf.as_strided((R, V), (ld, 1))
+
+
+@pytest.mark.parametrize("M", [5, 70])
+def test_product_offsets_past_32_bits(mt, M):  # noqa: F811
+    a, sa, w, sw = product_case(M, M, 200, 256, 1)
+    for out in (torch.bfloat16, torch.float32):
+        o = far_rows(M, 200, out, 4_500_000_000)
+        mt.gemm_fp8_block128(dev(a), dev(sa), dev(w), dev(sw), out=o)
+        check_product(o.contiguous(), a, sa, w, sw, 1)
+        del o
+    # a weight of 4.3 GB: its last rows
+    N, K = 700_001, 6144
+    wide = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    a, sa, w, sw = product_case(M, M, 300, K, 128)
+    wide[-300:] = dev(w)
+    scale = torch.ones(-(-N // 128), K // 128, device="cuda")
+    first = (N - 300) // 128 * 128                      # block rows of the last 300 weight rows
+    got = mt.gemm_fp8_block128(dev(a), dev(sa), wide, scale)
+    assert not got[:, :-300].any() and first > 0
+    check_product(got[:, -300:].contiguous(), a, sa, w, np.ones((3, K // 128), np.float32), 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_logits_and_table_offsets_past_32_bits(mt, dtype):  # noqa: F811
+    V, R = 50001, 6
+    c = Case(51, 2, 2, V, dtype, **ALL)
+    x = far_rows(R, V, dtype, 4_500_000_000)
+    x.copy_(c.logits)
+    probs, out = far_rows(R, V, torch.float32, 4_500_000_000), far_rows(R, V, torch.float32, 2_300_000_000)
+    table = torch.zeros(90_000, mt.token_counts_ld(V), dtype=torch.int16, device="cuda")      # 4.5e9 words
+    rows = torch.tensor([89_999, 45_000], dtype=torch.int32, device="cuda")
+    tokens, lens = dev(np.random.default_rng(5).integers(0, V, 6000).astype(np.int64)), [5000, 1000]
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.uint32)
+    mt.token_counts_build(tokens, u32(off), V, n_prompt=dev(np.array([100, 900])), counts=table, count_rows=rows)
+    mt.token_counts_accept(table, V, dev(c.draft), dev(np.array([2, 1], np.int32)), dev(np.array([7, 9])), count_rows=rows)
+    want = ologits.token_counts_build(np.zeros((2, table.shape[1]), np.int16), tokens.cpu().numpy(), off, V, [100, 900])
+    want = ologits.token_counts_accept(want, V, c.draft, np.array([2, 1]), np.array([7, 9]))
+    assert np.array_equal(table[rows.long()].cpu().numpy(), want) and int(torch.count_nonzero(table)) == np.count_nonzero(want)
+    c.counts = want
+    argmax = torch.empty(R, dtype=torch.int64, device="cuda")
+    c.call(mt, logits=x, counts=table, count_rows=rows, argmax=argmax, probs=probs, out_logits=out)
+    c.check(argmax, probs, out)
