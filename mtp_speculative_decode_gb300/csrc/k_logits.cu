@@ -577,8 +577,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2) process_logit
       if (idx != 0xffffffffu) atomicMin(&s_idx, idx);
     }
     // ---- the chunk's sum of exponentials, kept in place of the values
-    // log2(e) / T, finite so that equal values give 2^0 and positive so that a masked one gives 0
-    const float c2 = onehot ? 0.f : fminf(fmaxf(__fdiv_rn(1.44269504f, temp), 1e-38f), 3.4e38f);
+    // log2(e) / T, finite so that equal values give 2^0 and positive so that a masked one gives 0 (T = inf: the least float;
+    // the quotient of every finite T lies above it)
+    const float c2 = onehot ? 0.f : fminf(fmaxf(__fdiv_rn(1.44269504f, temp), 1.4e-45f), 3.4e38f);
     auto expo = [&](float x, float top) { return exp2_fast((x - top) * c2); };
     float sum = 0.f;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

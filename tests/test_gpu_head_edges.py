@@ -243,3 +243,26 @@ def test_logits_and_table_offsets_past_32_bits(mt, dtype):  # noqa: F811
     argmax = torch.empty(R, dtype=torch.int64, device="cuda")
     c.call(mt, logits=x, counts=table, count_rows=rows, argmax=argmax, probs=probs, out_logits=out)
     c.check(argmax, probs, out)
+
+
+def test_logits_very_high_temperatures(mt):  # noqa: F811
+    """Temperatures up to the largest float, with logits of that size: log2(e) / T is subnormal there (spacing 2^-149, at
+    least 2^-127.5 here, so that it is off by up to 2^-22.5 of its value), its product with a difference is not."""
+    V, temps = 64, [1e38, 1.3e38, 1.5e38, 2.5e38, 3.4e38]
+    rng = np.random.default_rng(61)
+    x = (rng.uniform(-1.6e38, 1.6e38, (len(temps), V))).astype(np.float32)
+    probs = torch.empty(len(temps), V, device="cuda")
+    mt.process_logits(dev(x), u32(np.arange(len(temps) + 1)), temperature=dev(np.array(temps, np.float32)), probs=probs)
+    for r, t in enumerate(np.array(temps, np.float32).astype(np.float64)):
+        d = (x[r].astype(np.float64) - x[r].max()) / t
+        want = np.exp(d) / np.exp(d).sum()
+        # three roundings, the constant and the subnormal quotient: below 2^-21.3 of an exponent of at most 3.2; then as
+        # in test_gpu_head.py
+        rel = np.expm1(2 * 2.0 ** -21.3 * 3.2) + 2.0 ** -22 + (V + 1) * 2.0 ** -23
+        assert (np.abs(probs[r].double().cpu().numpy() - want) <= 2 * rel * want).all()
+    t = torch.full((len(temps),), float("inf"), device="cuda")          # every open token alike
+    mask = dev(np.full((1, 2), 0x0F0F0F0F, np.int32))
+    mt.process_logits(dev(x), u32(np.arange(len(temps) + 1)), temperature=t, bitmask=mask,
+                      mask_rows=dev(np.zeros(len(temps), np.int32)), probs=probs)
+    got = probs.cpu().numpy().reshape(len(temps), -1, 8)
+    assert (got[:, :, 4:] == 0).all() and np.allclose(got[:, :, :4], 1 / 32, rtol=1e-6, atol=0)
