@@ -453,7 +453,9 @@ int mtpsd_topk_share_gather(const int32_t* step0_topk, const uint32_t* row_offse
  *           [ceil(N/128), K/128] (w_scale_rows 128: n' = n / 128, blocks of 128 x 128)
  *   out [M, N], out_dtype MTPSD_BF16 or MTPSD_F32, row stride ld_out (elements, >= N)
  * Each block's sum and the sum over the blocks are held in float32; the result is rounded
- * once to out_dtype.  The order of the sums depends on M, N and K only.
+ * once to out_dtype; the two scales are multiplied first, in float32.  The order of the sums depends on M, N, K and the
+ * device (how many of its SMs and clusters a launch finds), so that the same call repeats bit for bit on one device, not
+ * necessarily on another one.
  * K is a multiple of 128; a and w are 16-byte aligned, out to its element; M, N <= 2^31 - 256.
  * M = 0 or N = 0 launches nothing; K = 0 writes zeros.  A NaN code (0x7F, 0xFF) or a scale that is
  * not finite reaches the outputs of its own row m and column n and no others.
@@ -506,6 +508,8 @@ int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted,
  *   out_logits[r, t] = x
  *   argmax[r] = the lowest t of the largest x
  *   probs[r, t] = exp((x - max) / temperature[b]) / sum    (one-hot at argmax when temperature[b] is not > 0)
+ * The exponential is 2^y in float32, y = (x - max) (log2 e / temperature): y is off by less than 2^-22.3 of its value for
+ * temperatures of 1e-38 .. 1e38 (2^-21.3 above; positive ones below 4.24e-39 count as that), and a power below 2^-126 is 0.
  * Every input after row_offsets may be NULL and is then left out (repetition 1, temperature 1, ...); so may
  * each output, but not all three.  A row in which every x is -inf gets argmax -1 and probabilities 0 and is
  * flagged MTPSD_STATUS_EMPTY_ROW.  Entries of +inf share the mass equally.  A NaN that is not masked makes the row's
@@ -519,7 +523,7 @@ int mtpsd_token_counts_accept(const int64_t* draft, const int32_t* num_accepted,
  * hold a part of one.
  */
 typedef struct {
-  int32_t B;                   /* requests */
+  int32_t B;                   /* requests, at least 1 */
   int32_t R;                   /* rows that the arrays hold (>= row_offsets[B]; at most 2^24) */
   int64_t V;                   /* vocabulary */
   int32_t dtype;               /* MTPSD_F32 or MTPSD_BF16: logits */
