@@ -15,17 +15,21 @@
 // Roles (384 threads, one CTA per SM), as k_gemm_fp8.cu but:
 //   warps 0-7   epilogue: lanes 32 (w % 4) .. +31, of every 64 columns the 32 of half w / 4; 32 NP
 //               accumulators a thread (setmaxnreg moves the other warps' registers here: 208 against 88).
-//               Sixteen warps of half as many were slower (697 against 601 us at 768 x 154880 x 6144, before the
-//               scales were fetched ahead): a warp's waits and hand-offs cost the same whatever it adds.
+//               Sixteen warps of half as many were slower (697 against 601 us at 768 x 154880 x 6144): a warp's waits and
+//               hand-offs cost the same whatever it adds.  That was before the scales and probes were fetched a block
+//               ahead, and has not been measured since.
 //   warp 8      TMA producer of this CTA's operands; both CTAs' copies complete on the leader's barrier.
 //   warp 9      TMEM allocation; in the leader (even) CTA the MMA issue for the pair.
 //   warp 10     scales of this CTA's rows of a;  warp 11  scales of the tile's weight rows.
-// What bounds it: 768 x 154880 x 6144 takes 564 us, 2.6 PFLOP/s: the tensor cores are busy half of the time, and an epilogue
-// warp's 910 cycles a block set the pace (the reads of TMEM and the additions 400, the fetch of the next scales and barrier
-// 180, the hand-over of the buffer and the first read's latency most of the rest).  Reads of 16 columns at a time took 583
-// us; handing the buffer over in two halves, so that four are in flight, doubled the hand-overs (727 us); the next block's
-// first read in front of this block's last additions spilled (667 us).  Back to back on random codes the GPU draws 1385 of
-// its 1400 W (zeros: 755 W at the same speed), so that a shorter chain would give little.
+// What bounds it: 768 x 154880 x 6144 with quantised normal values takes 585 us as one call between kernels that draw
+// little (2070 MHz, 2.5 PFLOP/s) and 625 to 637 back to back, where the GPU is at its power limit (1389 of 1400 W, down to
+// 1702 MHz); 192 rows 205 and 223.  The tensor cores are busy half of the time, and an epilogue warp's 910 cycles a block
+// set the pace (the reads of TMEM and the additions 400, the fetch of the next scales and barrier 180, the hand-over of the
+// buffer and the first read's latency most of the rest).  On codes of one sign, 564 us as it is: reads of 16 columns at a
+// time 583; the buffer handed over in two halves, so that four are in flight, 727 (twice the hand-overs); the next block's
+// first read in front of this block's last additions 667 (spills).  Zeros for codes draw 755 W.
+// ROWS1: 192 x 154880 x 6144 takes 315 us, 768 rows 923, 256 x 6144 x 6144 24.0 (19.8 with 128 x 128 blocks): it reads TMEM
+// in the 16x256b shape, and a scale for every column.
 // With few tiles the blocks of K are split over up to 4 pairs of one cluster.
 #include <algorithm>
 
