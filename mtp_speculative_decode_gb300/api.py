@@ -41,7 +41,8 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: Optional[int] = None):
 def _empty(stream, *shape, dtype, device) -> torch.Tensor:
     """A new output.  torch's allocator hands a freed block out again in the order of the stream it was allocated on, so
     with a stream given the block has to be that stream's: one of the current stream may still be in use there, and after
-    the caller has dropped it the current stream could take it while the call still writes."""
+    the caller has dropped it the current stream could take it while the call still writes.  The current stream, where the
+    caller is, is recorded as a user of the block, so that it is not handed out while work queued there still reads it."""
     if stream is None:
         return torch.empty(*shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -49,7 +50,11 @@ def _empty(stream, *shape, dtype, device) -> torch.Tensor:
         # 0 and 1 are the handles of the default stream
         stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
+    return t
 
 
 class Workspace:

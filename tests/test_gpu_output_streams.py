@@ -3,7 +3,8 @@
 The allocator hands a freed block out again in the order of the stream that it belongs to.  An output from the current
 stream's memory would race twice: with work of the current stream that is still pending on the block when the call
 writes it, and with the next owner of the block when the caller drops the output before the call has run.  Both are
-made to happen here with a delay kernel on the stream that has to come second."""
+made to happen here with a delay kernel on the stream that has to come second, and so is the third: the call's stream
+takes the block of a dropped output that work queued on the current stream still reads."""
 import numpy as np
 import pytest
 import torch
@@ -78,6 +79,47 @@ def test_output_dropped_before_the_call_has_run(mt, name, raw):
     others = [torch.full_like(like, 3) for _ in range(3)]
     torch.cuda.synchronize()
     assert all((o == 3).all() for o in others)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", NAMES)
+def test_output_dropped_while_the_current_stream_reads_it(mt, name, raw):
+    call = calls(mt)[name]
+    side = torch.cuda.Stream()
+    handle = side.cuda_stream if raw else side
+    want = call(None)
+    torch.empty_like(want).copy_(want)
+    torch.full_like(want, 3)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = call(handle)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(DELAY)
+    seen = torch.empty_like(want).copy_(got)      # pending behind the delay
+    del got
+    with torch.cuda.stream(side):
+        others = [torch.full_like(want, 3) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(seen, want) and all((o == 3).all() for o in others)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_side_stream_inside_a_capture(mt, name):
+    call = calls(mt)[name]
+    want = call(None).clone()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        call(side)                       # dropped inside the capture
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        seen = got.clone()
+    for _ in range(3):
+        got.zero_(), seen.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(seen, want)
 
 
 def test_default_stream_by_its_handle(mt):
