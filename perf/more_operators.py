@@ -16,9 +16,11 @@ import torch
 
 own = False
 
-# latent rows of 416 bytes: 512 E2M1 codes (256 bytes, value 2i in the low half of byte i), 32 scales (one per 16 values,
-# unsigned, 5 bits of exponent and 3 of mantissa: code c is 2^(c//8 - 16) * (1 + c%8 / 8), but 0 is 0 and 255 is NaN), 64 bf16 rope values
+# latent rows of 416 bytes: 512 E2M1 codes (eight values to a 32-bit word: value 2j in its bits 4j .. 4j + 3, value 2j + 1 in
+# 16 + 4j .. 19 + 4j), 32 scales (one per 16 values, unsigned, 5 bits of exponent and 3 of mantissa: code c is
+# 2^(c//8 - 16) * (1 + c%8 / 8), but 0 is 0 and 255 is NaN), 64 bf16 rope values
 ROW4 = 416
+TO_NIBBLES, FROM_NIBBLES = (0, 2, 4, 6, 1, 3, 5, 7), (0, 4, 1, 5, 2, 6, 3, 7)
 MAGNITUDES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 SOFTMAX_SCALE = 1.0 / math.sqrt(576)
 
@@ -243,7 +245,7 @@ def _pack4(x):
     m = torch.zeros_like(y)
     for i, edge in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
         m += y >= edge if i % 2 else y > edge
-    nib = (m + 8 * torch.signbit(v)).to(torch.uint8).view(-1, 256, 2)
+    nib = (m + 8 * torch.signbit(v)).to(torch.uint8).view(-1, 64, 8)[:, :, TO_NIBBLES].view(-1, 256, 2)
     rope = x[:, 512:].to(torch.bfloat16).contiguous().view(torch.uint8)
     return torch.cat([nib[:, :, 0] | (nib[:, :, 1] << 4), code, rope], 1)
 
@@ -320,17 +322,19 @@ def _plain_tables(st):
     served = (need == 0) | (incl <= n_free)
     col = torch.arange(st["table"].shape[1], device="cuda")
     take = (n_free - 1 - (incl - need))[:, None] - (col - first[:, None])
-    mine = (col >= first[:, None]) & (col < (first + need)[:, None]) & served[:, None]
-    rest = torch.full_like(st["table"], -1) if old is None else st["table"]
-    table = torch.where(mine, st["free"][take.clamp(0, len(st["free"]) - 1)], rest)
+    mine = (col >= first[:, None]) & (col < (first + need)[:, None])
+    none = torch.full_like(st["table"], -1)
+    page_id = torch.where(served[:, None], st["free"][take.clamp(0, len(st["free"]) - 1)], none)
+    table = torch.where(mine, page_id, none if old is None else st["table"])
     off = st["offsets"].long()
     t = torch.arange(st["slots"].numel(), device="cuda")
     req = torch.searchsorted(off, t, right=True) - 1
     pos = new[req] - off[req + 1] + t
-    slot = table[req, pos // page].long() * page + pos % page
+    entry = table[req, pos // page].long()
+    slots = torch.where(entry >= 0, entry * page + pos % page, torch.full_like(pos, -1))
     lengths = torch.where(served, new, torch.zeros_like(new) if old is None else old)
     return dict(table=table, lengths=lengths, n_free=(n_free - (need * served).sum()).to(torch.int32),
-                slots=torch.where(served[req], slot, torch.full_like(slot, -1)), positions=pos)
+                slots=slots, positions=pos)
 
 
 def _rotate(x, cos_sin, start, rot, interleaved):
@@ -415,7 +419,7 @@ def _plain_mla4(st):
     R, n = rows.shape
     raw = st["cache"][rows.view(-1)]
     value = torch.tensor(MAGNITUDES + tuple(-v for v in MAGNITUDES), device="cuda")
-    nib = torch.stack([raw[:, :256] & 15, raw[:, :256] >> 4], 2).view(-1, 32, 16)
+    nib = torch.stack([raw[:, :256] & 15, raw[:, :256] >> 4], 2).view(-1, 64, 8)[:, :, FROM_NIBBLES].view(-1, 32, 16)
     c = torch.empty(R * n, 576, device="cuda")
     c[:, :512] = (value[nib.int()] * _scale4(raw[:, 256:288])[:, :, None]).view(-1, 512)
     c[:, 512:] = raw[:, 288:].contiguous().view(torch.bfloat16).float()
@@ -473,14 +477,16 @@ def _exact_tables(st):
         lo, hi = -(-old[b] // page), -(-new[b] // page)
         shut = shut or hi - lo > left
         ok = hi <= lo or not shut
-        if ok and hi > lo:
-            table[b, lo:hi] = torch.tensor(free[left - (hi - lo):left][::-1], dtype=torch.int32, device="cuda")
-            left -= hi - lo
+        if hi > lo:
+            ids = free[left - (hi - lo):left][::-1] if ok else [-1] * (hi - lo)
+            table[b, lo:hi] = torch.tensor(ids, dtype=torch.int32, device="cuda")
+            left -= hi - lo if ok else 0
         lengths.append(new[b] if ok else old[b])
         m = off[b + 1] - off[b]
         pos = torch.arange(new[b] - m, new[b], device="cuda")
         positions.append(pos)
-        slots.append(table[b].long()[pos // page] * page + pos % page if ok else torch.full_like(pos, -1))
+        entry = table[b].long()[pos // page]
+        slots.append(torch.where(entry < 0, -1, entry * page + pos % page))
     return dict(table=table, lengths=torch.tensor(lengths, device="cuda"),
                 n_free=torch.tensor([left], dtype=torch.int32, device="cuda"), slots=torch.cat(slots),
                 positions=torch.cat(positions))
@@ -546,8 +552,9 @@ def _exact_rope(st):
 
 def _unpack4(raw):
     """Rows of 416 bytes [n, 416] -> latent rows [n, 576] in 64 bits, from the bits."""
-    b = raw[:, :256].long()
-    nib = torch.stack([b % 16, b // 16], 2).view(len(raw), 512)
+    b = raw[:, :256].long().view(-1, 64, 4)
+    word = b[:, :, 0] + (b[:, :, 1] << 8) + (b[:, :, 2] << 16) + (b[:, :, 3] << 24)
+    nib = torch.stack([(word >> (4 * (v // 2) + 16 * (v % 2))) % 16 for v in range(8)], 2).view(len(raw), 512)
     e, m = (nib % 8) // 2, nib % 2
     mag = torch.where(e > 0, (1 + m.double() / 2) * torch.exp2(e.double() - 1), m.double() / 2)
     c = raw[:, 256:288].long()
