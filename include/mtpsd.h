@@ -58,6 +58,7 @@ extern "C" {
 #define MTPSD_FP8_E4M3 2
 #define MTPSD_FP8_DS_MLA 3  /* latent cache rows of 656 bytes: 512 E4M3 codes (four blocks of 128), the four
                                float32 block scales, the 64 rope values as bf16 ([P2] "草稿层 KV 的账") */
+#define MTPSD_FP4_MLA 4     /* latent cache rows of 416 bytes (mtpsd_pack_latent_fp4) */
 
 /* bits ORed into *dev_status */
 #define MTPSD_STATUS_INDEX_RANGE 1   /* a selected index outside 0..row_pos (skipped) */
@@ -65,6 +66,7 @@ extern "C" {
 #define MTPSD_STATUS_WAIT_TIMEOUT 4  /* a bounded device wait expired (kernel gave up) */
 #define MTPSD_STATUS_ROW_RANGE 8     /* a row position outside its request's pool rows (skipped) */
 #define MTPSD_STATUS_EMPTY_ROW 16    /* a logits row in which nothing is allowed (argmax -1, probabilities 0) */
+#define MTPSD_STATUS_NO_PAGES 32     /* a request that the free list has too few pages for (mtpsd_block_table_grow) */
 
 /* ------------------------------------------------------------------------
  * Ragged token merge.  [P4] "Token 合并:RaggedTokenMerger 与 ragged_token_merger"
@@ -252,8 +254,8 @@ typedef struct {
   int32_t d_v;             /* 512 */
   int32_t n_idx;           /* selected entries per row (row stride of idx) */
   int32_t n_append;        /* appended positions per row (0 = none) */
-  int32_t dtype;           /* MTPSD_BF16 or MTPSD_F32: q, latent and out; MTPSD_FP8_DS_MLA: bf16 q and out,
-                              latent rows of 656 bytes (the FP8 cache; dequantized tile by tile in shared memory) */
+  int32_t dtype;           /* MTPSD_BF16 or MTPSD_F32: q, latent and out; MTPSD_FP8_DS_MLA and MTPSD_FP4_MLA: bf16 q and out,
+                              latent rows of 656 or 416 bytes (dequantized tile by tile in shared memory) */
   float softmax_scale;
   int64_t row_pos_add;     /* added to row_pos[r] (draft step j of a shared loop passes j) */
   const void* q;           /* [R, H, d_latent] */
@@ -329,9 +331,9 @@ int mtpsd_accept_stochastic(const int64_t* draft, const float* draft_probs, cons
  * request b (pool rows cache_start[b] + dst_pos[b] + i); rejected rows are not
  * written.  Both caches of the layer move together.
  *   src_latent [B, W, 576] (latent_dtype: MTPSD_BF16 or MTPSD_F32), or [B, W, 656] packed
- *   bytes (MTPSD_FP8_DS_MLA)
+ *   bytes (MTPSD_FP8_DS_MLA), or [B, W, 416] (MTPSD_FP4_MLA)
  *   src_idxk [B, W, idx_dim] uint8, src_idxs [B, W] float32
- *   dst_latent [pool_tokens, 576], dst_idxk [pool_tokens, idx_dim], dst_idxs [pool_tokens]
+ *   dst_latent [pool_tokens, 576] (or rows of the packed bytes), dst_idxk [pool_tokens, idx_dim], dst_idxs [pool_tokens]
  *   cache_start [B], dst_pos [B] int64
  *   next_pos [B] int64 out, nullable: dst_pos[b] + num_accepted[b] + 1, the
  *   position of the next draft row.
@@ -382,7 +384,7 @@ int mtpsd_assign_cache_locs(const mtpsd_paged_kv* paged, int32_t B, const int64_
  * two slot lists of a request (rows whose source is their destination are
  * left alone; a chain of drafts, accept_index[b, i] = i, moves nothing).
  *   latent [pool_tokens, 576] (latent_dtype MTPSD_BF16 / MTPSD_F32) or [pool_tokens, 656]
- *   bytes (MTPSD_FP8_DS_MLA); idxk [pool_tokens, idx_dim] uint8 (idx_dim a multiple of 16,
+ *   bytes (MTPSD_FP8_DS_MLA) or [pool_tokens, 416] (MTPSD_FP4_MLA); idxk [pool_tokens, idx_dim] uint8 (idx_dim a multiple of 16,
  *   0 = none, idxk may then be NULL); idxs [pool_tokens] float32 or NULL.
  *   out_cache_loc [B, W] int64, accept_index [B, W] int32 (window columns), num_accepted [B] int32.
  * A window column outside [0, W) is skipped and flagged MTPSD_STATUS_INDEX_RANGE; a slot
@@ -556,6 +558,131 @@ typedef struct {
 } mtpsd_logits_args;
 
 int mtpsd_process_logits(const mtpsd_logits_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block tables from the requests' lengths (the tables that the paged calls read; [P2]
+ * "输入准备:prepare_for_draft" plans its slots from one), on the device: no length comes to the host.
+ *
+ * mtpsd_block_table_grow.  Request b (row b of the table) needs
+ *   need_b = max(0, ceil(new_len[b] / page_size) - ceil(old_len[b] / page_size))
+ * more pages, entries ceil(old_len[b] / page_size) .. of its row.  They come off the end of the free list in the
+ * requests' order, then the pages': the i-th page handed out is free_pages[n_free - 1 - i].  A request is served when
+ * need_0 + .. + need_b <= n_free (or need_b = 0); the first one that is not, and each later one that needs pages,
+ * gets -1 for every page that it needs and is flagged MTPSD_STATUS_NO_PAGES.
+ *   old_len NULL builds the tables anew: all entries of a row are written, -1 behind its pages.
+ *   lengths[b] (nullable) = new_len[b] where served, else old_len[b] (0 when built anew)
+ *   n_free_out[0] = n_free[0] - the pages handed out; free_pages is only read.
+ * A length that is negative or does not fit the row (new_len > bt_stride * page_size) leaves the request as it was (an
+ * empty row when built anew, lengths[b] = old_len[b]) and is flagged MTPSD_STATUS_ROW_RANGE; so is an n_free outside
+ * [0, free_cap], which is cut to it.  A negative entry of the free list is handed out as it is, flagged
+ * MTPSD_STATUS_INDEX_RANGE.  new_len < old_len keeps the pages (mtpsd_block_table_release returns them).
+ *
+ * With token_offsets the call also plans the slots of the step's tokens, request b's being tokens
+ * token_offsets[b] .. token_offsets[b+1]-1 (uint32, the prefix sums of mtpsd_merge_tokens), the last ones of its new length:
+ *   positions[t] = new_len[b] - (token_offsets[b+1] - token_offsets[b]) + (t - token_offsets[b])   (int64 [T], nullable)
+ *   slots[t]     = the pool slot of that position (int64 [T]), or -1 when it has none (flagged MTPSD_STATUS_ROW_RANGE)
+ * Tokens outside token_offsets[0] .. token_offsets[B]-1 (a padded batch) are left as they were; a token_offsets[B] past T is
+ * cut to it and flagged MTPSD_STATUS_ROW_RANGE.
+ *
+ * One launch, or two when n_free_out is n_free and the work is spread over several CTAs.  B <= 8192.
+ */
+typedef struct {
+  int32_t* block_table;          /* [B, bt_stride] page ids (device, written) */
+  int32_t bt_stride;             /* entries per request (>= 1) */
+  int32_t page_size;             /* tokens per page: a power of two, 1 .. 65536 */
+  int32_t B;                     /* requests, 0 .. 8192 */
+  int32_t free_cap;              /* entries of free_pages */
+  const int64_t* old_len;        /* [B] or NULL (tables built anew) */
+  const int64_t* new_len;        /* [B] */
+  const int32_t* free_pages;     /* [free_cap] page ids, the first n_free of them free */
+  const int32_t* n_free;         /* [1] */
+  int32_t* n_free_out;           /* [1]; may be n_free itself */
+  int64_t* lengths;              /* [B] or NULL; may be old_len itself */
+  const uint32_t* token_offsets; /* [B+1] or NULL (no slots planned) */
+  int64_t* slots;                /* [T] */
+  int64_t* positions;            /* [T] or NULL */
+  int64_t T;                     /* tokens that slots and positions hold (< 2^32) */
+  int32_t* dev_status;           /* nullable */
+} mtpsd_block_table_args;
+
+int mtpsd_block_table_grow(const mtpsd_block_table_args* args, void* stream);
+
+/* The pages behind keep_len[b] tokens (NULL: none are kept) go back to the free list, behind its n_free entries, in the
+ * requests' and then the pages' order: entries ceil(keep_len[b] / page_size) .. ceil(old_len[b] / page_size) - 1 of row b, which
+ * become -1 (an entry that is negative already is passed over).  n_free[0] grows by their number; a request whose pages do not
+ * fit free_cap keeps them and is flagged MTPSD_STATUS_WRITE_RANGE, as do those behind it.  Negative lengths, and old_len past
+ * the row, leave the request as it was, flagged MTPSD_STATUS_ROW_RANGE.  B <= 8192. */
+int mtpsd_block_table_release(int32_t* block_table, int32_t bt_stride, int32_t page_size, int32_t B, const int64_t* old_len,
+                              const int64_t* keep_len, int32_t* free_pages, int32_t free_cap, int32_t* n_free,
+                              int32_t* dev_status, void* stream);
+
+/* The slots and positions alone, over a table that is there (any B): as above with new_len = lengths.  mtpsd_assign_cache_locs
+ * is the form for windows of one width. */
+int mtpsd_slot_map(const mtpsd_paged_kv* paged, int32_t B, const uint32_t* token_offsets, const int64_t* lengths, int64_t T,
+                   int64_t* slots, int64_t* positions, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys for each head, and their position rotation, in one pass (the indexer's k_norm and rotation, [P3]
+ * "Indexer 的结构与计算流程"; the latent's norm and the rope parts of MLA, [P3] "稀疏 MLA 的前向路径"; per-head norms of any
+ * other attention).  For every token t and head, with x of D values:
+ *   MTPSD_NORM_RMS    y = x * 1 / sqrt(mean(x^2) + eps) * weight + bias
+ *   MTPSD_NORM_LAYER  y = (x - mean(x)) * 1 / sqrt(mean((x - mean(x))^2) + eps) * weight + bias
+ * over dims [0, norm_dim), the others unchanged; then dims [rot_start, rot_start + rot_dim) turned by the angles of
+ * positions[t]: pair i, with c = cos_sin[positions[t], i] and s = cos_sin[positions[t], rot_dim / 2 + i], becomes
+ *   (a, b) -> (a c - b s, a s + b c)
+ * where a and b are dims rot_start + i and rot_start + rot_dim / 2 + i, or rot_start + 2 i and + 2 i + 1 (interleaved).
+ * Everything is computed in float32 and rounded once, to the output's type:
+ *   MTPSD_BF16, MTPSD_F32   D values per head
+ *   MTPSD_FP8_E4M3          128 codes per head (D = 128) and a float32 scale, as mtpsd_quantize_fp8_block128 makes them: what
+ *                           mtpsd_indexer_topk reads as q, q_scale, k_cache and k_scale
+ *   MTPSD_FP8_DS_MLA, MTPSD_FP4_MLA   one latent cache row per token (one head, D = 576, rot_start 512 if anything is turned):
+ *                           the rows that mtpsd_pack_latent_fp8 / _fp4 make of the float32 values; keys only
+ * A key's output row is slots[t] of a cache of pool_tokens rows (slots NULL: row t); a slot outside it is skipped and flagged
+ * MTPSD_STATUS_WRITE_RANGE.  A token whose position is outside [0, n_pos) is left out (both sides), flagged
+ * MTPSD_STATUS_ROW_RANGE.  The output may be the input itself (same address, type and strides) when no slots are given; else they
+ * must not overlap.  Two tokens must not share a slot.
+ */
+#define MTPSD_NORM_NONE 0
+#define MTPSD_NORM_RMS 1
+#define MTPSD_NORM_LAYER 2
+typedef struct {
+  const void* x;            /* [T, heads, D], the D values of a head contiguous */
+  int64_t x_token_stride;   /* elements */
+  int64_t x_head_stride;    /* elements */
+  int32_t heads;            /* 1 .. 65535 */
+  int32_t D;                /* 1 .. 1024 */
+  int32_t dtype;            /* MTPSD_BF16 or MTPSD_F32: x */
+  int32_t norm;             /* MTPSD_NORM_* */
+  int32_t norm_dim;         /* 1 .. D */
+  int32_t rot_start;        /* first turned dim */
+  const float* weight;      /* [norm_dim] or NULL (1) */
+  const float* bias;        /* [norm_dim] or NULL (0) */
+  void* out;
+  int64_t out_token_stride; /* elements (bytes of the codes and of cache rows): from one token, or one cache row, to the next */
+  int64_t out_head_stride;  /* elements */
+  int32_t out_dtype;
+  float* scale;             /* [T, heads] (keys: [pool_tokens, heads]) for MTPSD_FP8_E4M3, else NULL */
+} mtpsd_head_side;
+
+/* q or k may be NULL.  rot_dim is even, 0 (no rotation; positions and cos_sin may then be NULL) .. D - rot_start.  x is aligned to
+ * its element, out too (16 bytes for cache rows, 4 for codes). */
+int mtpsd_norm_rope(const mtpsd_head_side* q, const mtpsd_head_side* k, int64_t T, const int64_t* positions,
+                    const float* cos_sin, int64_t n_pos, int32_t rot_dim, int32_t interleaved, float eps,
+                    const int64_t* slots, int64_t pool_tokens, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit latent cache rows: latent [T, 576] (MTPSD_BF16 or MTPSD_F32) -> rows of 416 bytes,
+ *   bytes 0 .. 255   the E2M1 codes of values 0 .. 511 (sign, then 0 0.5 1 1.5 2 3 4 6), eight values to a little-endian
+ *                    32-bit word: value 2j in its bits 4j .. 4j+3, value 2j + 1 in bits 16+4j .. 19+4j
+ *   bytes 256 .. 287 one scale per 16 values: code c is 2^(floor(c / 8) - 16) * (1 + (c mod 8) / 8), 0 is 0, 255 is NaN
+ *   bytes 288 .. 415 the 64 rope values 512 .. 575 as bf16 (round to nearest even)
+ * scale = amax / 6 rounded to the nearest scale (255 when a value is not finite), code = x / scale rounded to the nearest
+ * E2M1 value (both quotients in float32, ties to the even code; |x| > 6 scale gives 6).  A scale times a code is exact in bf16.
+ * Row t is written to packed row slots[t] (int64 [T]; NULL: row t) of pool_tokens; a slot outside it is skipped and flagged
+ * MTPSD_STATUS_WRITE_RANGE.  latent and packed are 16-byte aligned; two tokens must not share a slot.
+ */
+int mtpsd_pack_latent_fp4(const void* latent, int32_t dtype, int64_t T, uint8_t* packed, const int64_t* slots,
+                          int64_t pool_tokens, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------
  * Check of the device-side bounded wait (the source pages have no

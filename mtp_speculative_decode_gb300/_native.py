@@ -21,6 +21,11 @@ MTPSD_F32 = 0
 MTPSD_BF16 = 1
 MTPSD_FP8_E4M3 = 2
 MTPSD_FP8_DS_MLA = 3
+MTPSD_FP4_MLA = 4
+
+MTPSD_NORM_NONE = 0
+MTPSD_NORM_RMS = 1
+MTPSD_NORM_LAYER = 2
 
 NOALLOC_SCRATCH_BYTES = 16 << 20   # MTPSD_NOALLOC_SCRATCH_BYTES
 
@@ -29,6 +34,7 @@ STATUS_WRITE_RANGE = 2
 STATUS_WAIT_TIMEOUT = 4
 STATUS_ROW_RANGE = 8
 STATUS_EMPTY_ROW = 16
+STATUS_NO_PAGES = 32
 
 vp = C.c_void_p
 i32 = C.c_int32
@@ -70,6 +76,22 @@ class LogitsArgs(C.Structure):
     ]
 
 
+class BlockTableArgs(C.Structure):
+    _fields_ = [
+        ("block_table", vp), ("bt_stride", i32), ("page_size", i32), ("B", i32), ("free_cap", i32), ("old_len", vp),
+        ("new_len", vp), ("free_pages", vp), ("n_free", vp), ("n_free_out", vp), ("lengths", vp), ("token_offsets", vp),
+        ("slots", vp), ("positions", vp), ("T", i64), ("dev_status", vp),
+    ]
+
+
+class HeadSide(C.Structure):
+    _fields_ = [
+        ("x", vp), ("x_token_stride", i64), ("x_head_stride", i64), ("heads", i32), ("D", i32), ("dtype", i32),
+        ("norm", i32), ("norm_dim", i32), ("rot_start", i32), ("weight", vp), ("bias", vp), ("out", vp),
+        ("out_token_stride", i64), ("out_head_stride", i64), ("out_dtype", i32), ("scale", vp),
+    ]
+
+
 # name -> (restype, argtypes); every symbol include/mtpsd.h declares
 SIGNATURES = {
     "mtpsd_merge_tokens": (C.c_int, [vp, i64, vp, vp, i32, i32, vp, vp, vp]),
@@ -107,6 +129,12 @@ SIGNATURES = {
     "mtpsd_token_counts_build": (C.c_int, [vp, i64, vp, vp, i32, i64, vp, i64, i32, vp, vp, vp]),
     "mtpsd_token_counts_accept": (C.c_int, [vp, vp, vp, i32, i32, i64, vp, i64, i32, vp, vp, vp]),
     "mtpsd_process_logits": (C.c_int, [C.POINTER(LogitsArgs), vp]),
+    "mtpsd_block_table_grow": (C.c_int, [C.POINTER(BlockTableArgs), vp]),
+    "mtpsd_block_table_release": (C.c_int, [vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
+    "mtpsd_slot_map": (C.c_int, [C.POINTER(PagedKV), i32, vp, vp, i64, vp, vp, vp, vp]),
+    "mtpsd_norm_rope": (C.c_int, [C.POINTER(HeadSide), C.POINTER(HeadSide), i64, vp, vp, i64, i32, i32, C.c_float, vp, i64,
+                                  vp, vp]),
+    "mtpsd_pack_latent_fp4": (C.c_int, [vp, i32, i64, vp, vp, i64, vp, vp]),
     "mtpsd_check_bounded_wait": (C.c_int, [i64, vp, vp, vp]),
     "mtpsd_last_error": (C.c_char_p, []),
     "mtpsd_version": (i32, []),

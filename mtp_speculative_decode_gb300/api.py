@@ -313,11 +313,11 @@ def sparse_mla_decode(q, latent, cache_start, row_offsets, row_pos, idx, softmax
     then ignored and may be None)."""
     bf16 = q.dtype == torch.bfloat16
     _need(q, "q", torch.bfloat16 if bf16 else torch.float32, 3)
-    fp8kv = latent.dtype == torch.uint8     # the packed FP8 latent cache (656-byte rows)
-    if fp8kv:
+    packed = latent.dtype == torch.uint8     # a packed latent cache (656-byte FP8 or 416-byte 4-bit rows)
+    if packed:
         _need(latent, "latent", torch.uint8, 2)
-        if not bf16 or latent.shape[1] != 656:
-            raise ValueError("an FP8 latent cache needs bf16 queries and 656-byte rows")
+        if not bf16 or latent.shape[1] not in (656, 416):
+            raise ValueError("a packed latent cache needs bf16 queries and 656-byte (FP8) or 416-byte (4-bit) rows")
     else:
         _need(latent, "latent", q.dtype, 2)
     if cache_start is not None:
@@ -328,7 +328,7 @@ def sparse_mla_decode(q, latent, cache_start, row_offsets, row_pos, idx, softmax
     if append_base is not None:
         _need(append_base, "append_base", torch.int64, 1)
     R, H, DL = q.shape
-    dt = N.MTPSD_FP8_DS_MLA if fp8kv else (N.MTPSD_BF16 if bf16 else N.MTPSD_F32)
+    dt = _latent_dtype(latent)
     if out is None:
         out = _empty(stream, R, H, 512, dtype=q.dtype, device=q.device)
     nbytes = sparse_mla_workspace_size(R, H, idx.shape[1], n_append, dt)
@@ -398,8 +398,8 @@ def accept_stochastic(draft, draft_probs, target_probs, u_accept, u_sample, num_
 def kv_writeback(src_latent, src_idxk, src_idxs, num_accepted, dst_latent, dst_idxk, dst_idxs, cache_start, dst_pos,
                  next_pos=None, dev_status=None, stream=None):
     bf16 = src_latent.dtype == torch.bfloat16
-    fp8kv = src_latent.dtype == torch.uint8   # packed FP8 latent rows (656 bytes)
-    _need(src_latent, "src_latent", src_latent.dtype if fp8kv else (torch.bfloat16 if bf16 else torch.float32), 3)
+    packed = src_latent.dtype == torch.uint8   # packed latent rows (656 or 416 bytes)
+    _need(src_latent, "src_latent", src_latent.dtype if packed else (torch.bfloat16 if bf16 else torch.float32), 3)
     _need(dst_latent, "dst_latent", src_latent.dtype, 2)
     _need(num_accepted, "num_accepted", torch.int32, 1)
     _need(cache_start, "cache_start", torch.int64, 1)
@@ -415,7 +415,7 @@ def kv_writeback(src_latent, src_idxk, src_idxs, num_accepted, dst_latent, dst_i
         _need(dst_idxs, "dst_idxs", torch.float32)
     check("mtpsd_kv_writeback", lib().mtpsd_kv_writeback(
         _ptr(src_latent), _ptr(src_idxk), _ptr(src_idxs), B, W,
-        N.MTPSD_FP8_DS_MLA if fp8kv else (N.MTPSD_BF16 if bf16 else N.MTPSD_F32), idx_dim,
+        _latent_dtype(src_latent), idx_dim,
         _ptr(num_accepted), _ptr(dst_latent), _ptr(dst_idxk), _ptr(dst_idxs), _ptr(cache_start), _ptr(dst_pos),
         dst_latent.shape[0], _ptr(next_pos), _ptr(dev_status), _stream(stream)))
     return next_pos
@@ -447,7 +447,7 @@ def topk_share_gather(step0_topk, row_offsets, num_accepted=None, shared_idx=Non
 
 def _latent_dtype(t):
     if t.dtype == torch.uint8:
-        return N.MTPSD_FP8_DS_MLA
+        return N.MTPSD_FP4_MLA if t.shape[-1] == 416 else N.MTPSD_FP8_DS_MLA
     return N.MTPSD_BF16 if t.dtype == torch.bfloat16 else N.MTPSD_F32
 
 
@@ -750,3 +750,229 @@ def process_logits(logits, row_offsets, draft=None, counts=None, count_rows=None
                      p_probs, ld_probs, p_out, ld_out, _status_ptr(dev_status, dev))
     check("mtpsd_process_logits", lib().mtpsd_process_logits(C.byref(a), _raw_stream(stream, dev)))
     return argmax
+
+
+# --------------------------------------------------------------------------- filling the caches
+
+def _opt(t, name: str, dev: int, dtype, ndim: int, numel: Optional[int] = None):
+    """The address of an optional tensor (None stays None), checked like _tensor."""
+    if t is None:
+        return None
+    p = _tensor(t, name, dev, dtype, ndim)
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
+    return p
+
+
+def block_table_grow(block_table, page_size: int, new_len, free_pages, n_free, old_len=None, lengths=None, n_free_out=None,
+                     token_offsets=None, slots=None, positions=None, dev_status=None, stream=None):
+    """Block tables from the requests' lengths: request b of block_table [B, n] int32 gets the pages between old_len[b] and
+    new_len[b] tokens (int64 [B]; without old_len the tables are built anew) off the end of free_pages [cap] int32, of which
+    n_free [1] int32 are free; n_free_out (in place without it) receives what is left.  Requests that the list has too few
+    pages for get -1 (STATUS_NO_PAGES).  lengths [B] int64 receives what each request has pages for.
+
+    With token_offsets [B+1] uint32 (request b's tokens of this step, the last of its new length), slots [T] int64 and
+    positions [T] int64 (optional) receive each token's pool slot (-1: none) and position.  Returns lengths."""
+    dev = _current(block_table, "block_table")
+    pt = _tensor(block_table, "block_table", dev, torch.int32, 2)
+    B, width = block_table.shape
+    pn = _opt(new_len, "new_len", dev, torch.int64, 1, B)
+    if pn is None:
+        raise TypeError("new_len must be a torch tensor")
+    po = _opt(old_len, "old_len", dev, torch.int64, 1, B)
+    pf = _tensor(free_pages, "free_pages", dev, torch.int32, 1)
+    pc = _opt(n_free, "n_free", dev, torch.int32, 1, 1)
+    if pc is None:
+        raise TypeError("n_free must be a torch tensor")
+    pco = pc if n_free_out is None else _opt(n_free_out, "n_free_out", dev, torch.int32, 1, 1)
+    if lengths is None:
+        lengths = _empty(stream, B, dtype=torch.int64, device=block_table.device)
+    pl = _opt(lengths, "lengths", dev, torch.int64, 1, B)
+    pto = ps = pp = None
+    T = 0
+    if token_offsets is not None:
+        if slots is None:
+            raise ValueError("token_offsets needs slots")
+        pto = _opt(token_offsets, "token_offsets", dev, torch.uint32, 1, B + 1)
+        ps = _tensor(slots, "slots", dev, torch.int64, 1)
+        T = slots.numel()
+        pp = _opt(positions, "positions", dev, torch.int64, 1, T)
+    elif slots is not None or positions is not None:
+        raise ValueError("slots and positions need token_offsets")
+    # in the order of the structure's fields
+    a = N.BlockTableArgs(pt, width, int(page_size), B, free_pages.numel(), po, pn, pf, pc, pco, pl, pto, ps, pp, T,
+                         _status_ptr(dev_status, dev))
+    check("mtpsd_block_table_grow", lib().mtpsd_block_table_grow(C.byref(a), _raw_stream(stream, dev)))
+    return lengths
+
+
+def block_table_release(block_table, page_size: int, old_len, free_pages, n_free, keep_len=None, dev_status=None, stream=None):
+    """Returns the pages behind keep_len[b] tokens (none are kept without it) of each request to the free list: behind its
+    n_free entries, which grow in place; their table entries become -1."""
+    dev = _current(block_table, "block_table")
+    pt = _tensor(block_table, "block_table", dev, torch.int32, 2)
+    B, width = block_table.shape
+    po = _opt(old_len, "old_len", dev, torch.int64, 1, B)
+    if po is None:
+        raise TypeError("old_len must be a torch tensor")
+    pk = _opt(keep_len, "keep_len", dev, torch.int64, 1, B)
+    pf = _tensor(free_pages, "free_pages", dev, torch.int32, 1)
+    pc = _opt(n_free, "n_free", dev, torch.int32, 1, 1)
+    if pc is None:
+        raise TypeError("n_free must be a torch tensor")
+    check("mtpsd_block_table_release", lib().mtpsd_block_table_release(
+        pt, width, int(page_size), B, po, pk, pf, free_pages.numel(), pc, _status_ptr(dev_status, dev),
+        _raw_stream(stream, dev)))
+
+
+def slot_map(block_table, page_size: int, token_offsets, lengths, slots, positions=None, dev_status=None, stream=None):
+    """slots [T] int64 (and positions [T] int64) of ragged tokens: request b's are tokens token_offsets[b] ..
+    token_offsets[b+1]-1 (uint32 [B+1]), the last ones of its lengths[b] (int64) tokens.  Returns slots."""
+    dev = _current(block_table, "block_table")
+    pt = _tensor(block_table, "block_table", dev, torch.int32, 2)
+    B, width = block_table.shape
+    pto = _opt(token_offsets, "token_offsets", dev, torch.uint32, 1, B + 1)
+    pl = _opt(lengths, "lengths", dev, torch.int64, 1, B)
+    if pto is None or pl is None:
+        raise TypeError("token_offsets and lengths must be torch tensors")
+    ps = _tensor(slots, "slots", dev, torch.int64, 1)
+    T = slots.numel()
+    pp = _opt(positions, "positions", dev, torch.int64, 1, T)
+    pk = N.PagedKV(pt, width, int(page_size))
+    check("mtpsd_slot_map", lib().mtpsd_slot_map(C.byref(pk), B, pto, pl, T, ps, pp, _status_ptr(dev_status, dev),
+                                                 _raw_stream(stream, dev)))
+    return slots
+
+
+_NORMS = {None: N.MTPSD_NORM_NONE, "rms": N.MTPSD_NORM_RMS, "layer": N.MTPSD_NORM_LAYER}
+_TYPES = {torch.bfloat16: N.MTPSD_BF16, torch.float32: N.MTPSD_F32}
+
+
+def _head_side(t, name, dev, norm, weight, bias, norm_dim, rot_start, out, scale, pool, stream):
+    """One side of norm_rope: (HeadSide, out).  out: [T (pool), heads, D] (or without the head dimension for one head), codes or
+    cache rows as uint8."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}, is on {t.device}")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [T, heads, D] or [T, D]")
+    T, D = t.shape[0], t.shape[-1]
+    heads = t.shape[1] if t.dim() == 3 else 1
+    st = t.stride()
+    if D > 1 and t.numel() and st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    if norm not in _NORMS:
+        raise ValueError(f"{name}_norm must be None, 'rms' or 'layer'")
+    nd = D if norm_dim is None else int(norm_dim)
+    pw = _opt(weight, f"{name}_weight", dev, torch.float32, 1, nd)
+    pb = _opt(bias, f"{name}_bias", dev, torch.float32, 1, nd)
+    rows = T if pool is None else pool
+    if out is None:
+        if pool is not None:
+            raise ValueError(f"slots need {name}_out, the cache")
+        out = _empty(stream, *t.shape, dtype=t.dtype, device=t.device)
+    if not isinstance(out, torch.Tensor):
+        raise TypeError(f"{name}_out must be a torch tensor")
+    if out.get_device() != dev:
+        raise ValueError(f"{name}_out must be a CUDA tensor on the current device cuda:{dev}, is on {out.device}")
+    so = out.stride()
+    packed = out.dtype == torch.uint8 and D == 576 and out.dim() == 2 and out.shape[1] in (656, 416)
+    if packed:
+        if out.shape[0] != rows or heads != 1:
+            raise ValueError(f"{name}_out must have {rows} cache rows, of one head")
+        dtype, hs = _latent_dtype(out), 0
+    else:
+        if out.dtype == torch.uint8:
+            dtype = N.MTPSD_FP8_E4M3
+        elif out.dtype in _TYPES:
+            dtype = _TYPES[out.dtype]
+        else:
+            raise TypeError(f"{name}_out must be bfloat16, float32 or uint8, got {out.dtype}")
+        if tuple(out.shape) != (rows, heads, D) and not (heads == 1 and tuple(out.shape) == (rows, D)):
+            raise ValueError(f"{name}_out must be [{rows}, {heads}, {D}], got {list(out.shape)}")
+        hs = so[1] if out.dim() == 3 else D
+    if out.numel() and so[-1] != 1 and out.shape[-1] > 1:
+        raise ValueError(f"{name}_out must have contiguous rows")
+    if rows > 1 and out.numel():
+        # heads inside their row, rows apart
+        if (heads > 1 and hs < D) or so[0] < (out.shape[1] if packed else D) or \
+                not (so[0] >= (heads - 1) * hs + D or packed or hs >= (rows - 1) * so[0] + D):
+            raise ValueError(f"{name}_out must have heads that do not overlap")
+    psc = None
+    if dtype == N.MTPSD_FP8_E4M3:
+        if scale is None:
+            raise ValueError(f"{name}_out of codes needs {name}_scale")
+        psc = _tensor(scale, f"{name}_scale", dev, torch.float32, scale.dim())
+        if scale.numel() != rows * heads:
+            raise ValueError(f"{name}_scale must have {rows * heads} entries")
+    side = N.HeadSide(t.data_ptr(), st[0], st[1] if t.dim() == 3 else D, heads, D, _TYPES[t.dtype], _NORMS[norm], nd,
+                      int(rot_start), pw, pb, out.data_ptr(), so[0], hs, dtype, psc)
+    return side, out
+
+
+def norm_rope(positions, cos_sin, q=None, k=None, q_norm=None, q_weight=None, q_bias=None, q_norm_dim=None, q_rot_start=0,
+              q_out=None, q_scale=None, k_norm=None, k_weight=None, k_bias=None, k_norm_dim=None, k_rot_start=0, k_out=None,
+              k_scale=None, slots=None, interleaved=False, eps=1e-6, dev_status=None, stream=None):
+    """The norms of queries q [T, heads, D] and keys k [T, heads, D] (or [T, D]; bf16 or float32, any token and head strides)
+    for each head, and their rotation by the angles of positions [T] int64, in one pass.
+
+    q_norm, k_norm: None, "rms" or "layer", over dims 0 .. norm_dim - 1 (all without it), with float32 weight and bias.
+    cos_sin [n_pos, rot_dim] float32: the cosines and then the sines of each position's rot_dim / 2 angles, which turn dims rot_start ..
+    rot_start + rot_dim - 1: dim i with dim i + rot_dim / 2, or neighbours (interleaved).  positions and cos_sin None: no rotation.
+
+    Outputs: like the input without one given; bf16 or float32 [T, heads, D]; uint8 codes [T, heads, 128] with a float32 scale
+    [T, heads] (what indexer_topk reads).  k_out may be a cache of `pool` rows with slots [T] int64: those types, or uint8 latent rows
+    [pool, 656] (FP8) or [pool, 416] (4 bits).  Returns (q_out, k_out)."""
+    if q is None and k is None:
+        raise ValueError("give q, k or both")
+    first, name = (q, "q") if q is not None else (k, "k")
+    dev = _current(first, name)
+    T = first.shape[0]
+    if q is not None and k is not None and k.shape[0] != T:
+        raise ValueError("q and k must have the same tokens")
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("give positions and cos_sin together or neither")
+    pp = _opt(positions, "positions", dev, torch.int64, 1, T)
+    pcs = _opt(cos_sin, "cos_sin", dev, torch.float32, 2)
+    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    psl = _opt(slots, "slots", dev, torch.int64, 1, T)
+    pool = None
+    if slots is not None:
+        if k is None or not isinstance(k_out, torch.Tensor):
+            raise ValueError("slots need k and k_out, the cache")
+        pool = k_out.shape[0]
+    sq = sk = None
+    if q is not None:
+        sq, q_out = _head_side(q, "q", dev, q_norm, q_weight, q_bias, q_norm_dim, q_rot_start, q_out, q_scale, None, stream)
+    if k is not None:
+        sk, k_out = _head_side(k, "k", dev, k_norm, k_weight, k_bias, k_norm_dim, k_rot_start, k_out, k_scale, pool, stream)
+    check("mtpsd_norm_rope", lib().mtpsd_norm_rope(
+        _byref(sq), _byref(sk), T, pp, pcs, n_pos, rot, 1 if interleaved else 0, float(eps), psl, 0 if pool is None else pool,
+        _status_ptr(dev_status, dev), _raw_stream(stream, dev)))
+    return q_out, k_out
+
+
+def pack_latent_fp4(latent, packed=None, slots=None, dev_status=None, stream=None):
+    """latent [T, 576] bf16 or float32 -> 4-bit latent cache rows of 416 bytes: packed [T, 416] uint8, or rows slots [T] int64 of
+    the cache packed [pool, 416].  Returns packed."""
+    dev = _current(latent, "latent")
+    if latent.dtype not in _TYPES:
+        raise TypeError(f"latent must be bfloat16 or float32, got {latent.dtype}")
+    pl = _tensor(latent, "latent", dev, latent.dtype, 2)
+    T = latent.shape[0]
+    if latent.shape[1] != 576:
+        raise ValueError("latent rows must have 576 values")
+    psl = _opt(slots, "slots", dev, torch.int64, 1, T)
+    if packed is None:
+        if slots is not None:
+            raise ValueError("slots need packed, the cache")
+        packed = _empty(stream, T, 416, dtype=torch.uint8, device=latent.device)
+    pk = _tensor(packed, "packed", dev, torch.uint8, 2)
+    if packed.shape[1] != 416 or (slots is None and packed.shape[0] != T):
+        raise ValueError("packed must be [T, 416], or [pool, 416] with slots")
+    check("mtpsd_pack_latent_fp4", lib().mtpsd_pack_latent_fp4(
+        pl, _TYPES[latent.dtype], T, pk, psl, packed.shape[0], _status_ptr(dev_status, dev), _raw_stream(stream, dev)))
+    return packed

@@ -50,7 +50,7 @@ extern "C" {
 
 const char* mtpsd_last_error(void) { return g_err; }
 
-int32_t mtpsd_version(void) { return 103; }
+int32_t mtpsd_version(void) { return 104; }
 
 int mtpsd_merge_tokens(const int64_t* prompt_tokens, int64_t S, const uint32_t* prompt_offsets,
                        const int64_t* draft_tokens, int32_t B, int32_t K, int64_t* merged_tokens,
@@ -275,10 +275,10 @@ int mtpsd_sparse_mla_decode_paged(const mtpsd_mla_args* a, const mtpsd_paged_kv*
   if (a->d_latent != 576 || a->d_v != 512)
     return fail(MTPSD_EUNSUPPORTED, "sparse_mla_decode: d_latent must be 576 and d_v 512");
   if ((int64_t)a->n_idx + a->n_append > 65536) return fail(MTPSD_EUNSUPPORTED, "sparse_mla_decode: more than 65536 positions per row");
-  if (a->dtype == MTPSD_BF16 || a->dtype == MTPSD_FP8_DS_MLA) {
+  if (a->dtype == MTPSD_BF16 || a->dtype == MTPSD_FP8_DS_MLA || a->dtype == MTPSD_FP4_MLA) {
     if (a->n_heads % 16) return fail(MTPSD_EUNSUPPORTED, "sparse_mla_decode: bf16 needs n_heads % 16 == 0");
   } else if (a->dtype != MTPSD_F32) {
-    return fail(MTPSD_EUNSUPPORTED, "sparse_mla_decode: dtype must be MTPSD_BF16, MTPSD_FP8_DS_MLA or MTPSD_F32");
+    return fail(MTPSD_EUNSUPPORTED, "sparse_mla_decode: dtype must be MTPSD_BF16, MTPSD_FP8_DS_MLA, MTPSD_FP4_MLA or MTPSD_F32");
   }
   if (a->n_append > 0 && !a->append_base) return fail(MTPSD_EINVAL, "sparse_mla_decode: n_append > 0 needs append_base");
   if (a->R == 0) return MTPSD_OK;
@@ -329,7 +329,8 @@ int mtpsd_kv_writeback(const void* src_latent, const uint8_t* src_idxk, const fl
   if (latent_dtype == MTPSD_BF16) lat_bytes = 576 * 2;
   else if (latent_dtype == MTPSD_F32) lat_bytes = 576 * 4;
   else if (latent_dtype == MTPSD_FP8_DS_MLA) lat_bytes = 656;
-  else return fail(MTPSD_EUNSUPPORTED, "kv_writeback: latent dtype must be MTPSD_BF16, MTPSD_F32 or MTPSD_FP8_DS_MLA");
+  else if (latent_dtype == MTPSD_FP4_MLA) lat_bytes = 416;
+  else return fail(MTPSD_EUNSUPPORTED, "kv_writeback: latent dtype must be MTPSD_BF16, MTPSD_F32, MTPSD_FP8_DS_MLA or MTPSD_FP4_MLA");
   if (idx_dim != 0 && idx_dim % 16) return fail(MTPSD_EUNSUPPORTED, "kv_writeback: idx_dim must be a multiple of 16");
   if (B == 0) return MTPSD_OK;
   if (!src_latent || !dst_latent || !num_accepted || !cache_start || !dst_pos) return fail(MTPSD_EINVAL, "kv_writeback: null pointer");
@@ -351,7 +352,8 @@ int mtpsd_kv_writeback_slots(const void* src_latent, const uint8_t* src_idxk, co
   if (latent_dtype == MTPSD_BF16) lat_bytes = 576 * 2;
   else if (latent_dtype == MTPSD_F32) lat_bytes = 576 * 4;
   else if (latent_dtype == MTPSD_FP8_DS_MLA) lat_bytes = 656;
-  else return fail(MTPSD_EUNSUPPORTED, "kv_writeback_slots: latent dtype must be MTPSD_BF16, MTPSD_F32 or MTPSD_FP8_DS_MLA");
+  else if (latent_dtype == MTPSD_FP4_MLA) lat_bytes = 416;
+  else return fail(MTPSD_EUNSUPPORTED, "kv_writeback_slots: latent dtype must be MTPSD_BF16, MTPSD_F32, MTPSD_FP8_DS_MLA or MTPSD_FP4_MLA");
   if (idx_dim != 0 && idx_dim % 16) return fail(MTPSD_EUNSUPPORTED, "kv_writeback_slots: idx_dim must be a multiple of 16");
   if (B == 0) return MTPSD_OK;
   if (!src_latent || !dst_latent || !num_accepted || !dst_slots) return fail(MTPSD_EINVAL, "kv_writeback_slots: null pointer");
@@ -387,7 +389,8 @@ int mtpsd_kv_move_accepted(void* latent, int32_t latent_dtype, uint8_t* idxk, in
   if (latent_dtype == MTPSD_BF16) lat_bytes = 576 * 2;
   else if (latent_dtype == MTPSD_F32) lat_bytes = 576 * 4;
   else if (latent_dtype == MTPSD_FP8_DS_MLA) lat_bytes = 656;
-  else return fail(MTPSD_EUNSUPPORTED, "kv_move_accepted: latent dtype must be MTPSD_BF16, MTPSD_F32 or MTPSD_FP8_DS_MLA");
+  else if (latent_dtype == MTPSD_FP4_MLA) lat_bytes = 416;
+  else return fail(MTPSD_EUNSUPPORTED, "kv_move_accepted: latent dtype must be MTPSD_BF16, MTPSD_F32, MTPSD_FP8_DS_MLA or MTPSD_FP4_MLA");
   if (idx_dim < 0 || idx_dim > 512 || idx_dim % 16) return fail(MTPSD_EUNSUPPORTED, "kv_move_accepted: idx_dim must be a multiple of 16 up to 512");
   if (B == 0) return MTPSD_OK;
   if (!latent || !out_cache_loc || !accept_index || !num_accepted || (idx_dim && !idxk))

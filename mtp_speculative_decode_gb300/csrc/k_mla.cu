@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "latent4.cuh"
 
 namespace mtpsd {
 
@@ -89,9 +90,14 @@ struct MlaSplit {
   int64_t per_split;   // positions per split (multiple of MLA_NT)
 };
 
-// Shared memory layout of the bf16 kernel (FP8KV adds the staging tiles of the packed rows).
+// Latent rows of the bf16 kernel: bf16, or packed in 8 or 4 bits (their bytes per row, the staging tiles' stride).
+enum { KV_BF16 = 0, KV_FP8 = 1, KV_FP4 = 2 };
 constexpr int MLA_FP8_ROW = 656;          // packed FP8 latent row: 512 codes, 4 float32 scales, 64 bf16 rope
-template <bool FP8KV>
+template <int KV>
+constexpr int mla_row_bytes() { return KV == KV_FP4 ? lat4::ROW : MLA_FP8_ROW; }
+
+// Shared memory layout of the bf16 kernel (packed rows add their staging tiles).
+template <int KV>
 struct MlaSmemT {
   static constexpr int Q = 0;                                     // [64][ROWB]
   static constexpr int C = Q + MLA_HG * MLA_ROWB;                 // [2][32][ROWB]
@@ -99,10 +105,9 @@ struct MlaSmemT {
   static constexpr int RED = P + MLA_HG * MLA_PROWB;              // [2][64] float
   static constexpr int LSUM = RED + 2 * MLA_HG * 4;               // [2][64] float
   static constexpr int ROWS = LSUM + 2 * MLA_HG * 4;              // [MAX_SPLIT] int64
-  static constexpr int STG = ROWS + MLA_MAX_SPLIT * 8;            // FP8KV: [2][32][656] packed rows
-  static constexpr int BYTES = STG + (FP8KV ? 2 * MLA_NT * MLA_FP8_ROW : 0);
+  static constexpr int STG = ROWS + MLA_MAX_SPLIT * 8;            // packed rows: [2][32][row bytes]
+  static constexpr int BYTES = STG + (KV != KV_BF16 ? 2 * MLA_NT * mla_row_bytes<KV>() : 0);
 };
-using MlaSmem = MlaSmemT<false>;
 
 // One tile of packed FP8 rows (staging) -> bf16 rows of the compute tile: value = code * block scale
 // (E4M3 -> f16 is exact; the product is formed in float32 and rounded to bf16), rope copied.
@@ -130,10 +135,26 @@ __device__ __forceinline__ void mla_dequant_tile(const uint8_t* stg, uint8_t* c)
   }
 }
 
-template <bool FP8KV>
+// The same for 4-bit rows (exact in bf16): a word of eight codes per thread and step.
+__device__ __forceinline__ void mla_dequant4_tile(const uint8_t* stg, uint8_t* c) {
+  for (int w = threadIdx.x; w < MLA_NT * 64; w += blockDim.x) {
+    const int i = w >> 6, grp = w & 63;
+    const uint8_t* src = stg + i * lat4::ROW;
+    uint32_t out[4];
+    lat4::decode8(*(const uint32_t*)(src + grp * 4), lat4::scale_value(src[lat4::OFF_SCALE + (grp >> 1)]), out);
+    *(uint4*)(c + i * MLA_ROWB + grp * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+  for (int w = threadIdx.x; w < MLA_NT * 8; w += blockDim.x) {    // rope: 8 chunks of 16 bytes per row
+    const int i = w >> 3, ch = w & 7;
+    *(uint4*)(c + i * MLA_ROWB + 1024 + ch * 16) = *(const uint4*)(stg + i * lat4::ROW + lat4::OFF_ROPE + ch * 16);
+  }
+}
+
+template <int KV>
 __global__ void __launch_bounds__(256, 1) sparse_mla_bf16_kernel(MlaPlan p, MlaSplit sp, float* __restrict__ part_o,
                                                                   float* __restrict__ part_ml) {
-  using MlaSmem = MlaSmemT<FP8KV>;
+  using MlaSmem = MlaSmemT<KV>;
+  constexpr int ROWP = mla_row_bytes<KV>();   // packed rows
   griddep_wait();                // the previous kernel's writes are visible from here on
   griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t sm[];
@@ -172,13 +193,13 @@ __global__ void __launch_bounds__(256, 1) sparse_mla_bf16_kernel(MlaPlan p, MlaS
 
   const __nv_bfloat16* lat = (const __nv_bfloat16*)p.latent;
   auto gather = [&](int tile, int buf) {
-    if constexpr (FP8KV) {   // packed rows into the staging tile (invalid rows zero-filled: scale 0)
+    if constexpr (KV != KV_BF16) {   // packed rows into the staging tile (invalid rows zero-filled: scale 0)
       const uint8_t* lat8 = (const uint8_t*)p.latent;
-      for (int c = tid; c < MLA_NT * (MLA_FP8_ROW / 16); c += blockDim.x) {
-        int i = c / (MLA_FP8_ROW / 16), ch = c % (MLA_FP8_ROW / 16);
+      for (int c = tid; c < MLA_NT * (ROWP / 16); c += blockDim.x) {
+        int i = c / (ROWP / 16), ch = c % (ROWP / 16);
         int64_t row = rows_s[(int64_t)tile * MLA_NT + i];
-        const void* src = row >= 0 ? (const void*)(lat8 + row * MLA_FP8_ROW + ch * 16) : (const void*)lat8;
-        cp_async16(smem_u32(sm + MlaSmem::STG + (buf * MLA_NT + i) * MLA_FP8_ROW + ch * 16), src, row >= 0);
+        const void* src = row >= 0 ? (const void*)(lat8 + row * ROWP + ch * 16) : (const void*)lat8;
+        cp_async16(smem_u32(sm + MlaSmem::STG + (buf * MLA_NT + i) * ROWP + ch * 16), src, row >= 0);
       }
     } else {
       for (int c = tid; c < MLA_NT * (MLA_DL / 8); c += blockDim.x) {
@@ -208,8 +229,10 @@ __global__ void __launch_bounds__(256, 1) sparse_mla_bf16_kernel(MlaPlan p, MlaS
       cp_async_wait<0>();
     }
     __syncthreads();
-    if constexpr (FP8KV) {
-      mla_dequant_tile(sm + MlaSmem::STG + buf * MLA_NT * MLA_FP8_ROW, sm + MlaSmem::C + buf * MLA_NT * MLA_ROWB);
+    if constexpr (KV != KV_BF16) {
+      const uint8_t* stg = sm + MlaSmem::STG + buf * MLA_NT * ROWP;
+      if constexpr (KV == KV_FP8) mla_dequant_tile(stg, sm + MlaSmem::C + buf * MLA_NT * MLA_ROWB);
+      else mla_dequant4_tile(stg, sm + MlaSmem::C + buf * MLA_NT * MLA_ROWB);
       __syncthreads();
     }
 
@@ -593,6 +616,14 @@ size_t mla_workspace_bytes(int R, int H, int n_idx, int n_append, int dtype) {
   return n;
 }
 
+template <int KV>
+static bool launch_portable(const MlaPlan& p, const MlaSplit& sp, dim3 grid, float* part_o, float* part_ml, cudaStream_t st,
+                            std::atomic<uint64_t>& attr) {
+  if (!set_smem_limit_once(sparse_mla_bf16_kernel<KV>, MlaSmemT<KV>::BYTES, attr)) return false;
+  launch_k(sparse_mla_bf16_kernel<KV>, grid, 256, MlaSmemT<KV>::BYTES, st, p, sp, part_o, part_ml);
+  return true;
+}
+
 int launch_sparse_mla(const MlaPlan& p, cudaStream_t st) {
   if (p.R == 0) return MTPSD_OK;
   // the kernel is decided once, and the split plan is that kernel's
@@ -627,19 +658,20 @@ int launch_sparse_mla(const MlaPlan& p, cudaStream_t st) {
     }
     return MTPSD_OK;
   }
-  if (p.dtype == MTPSD_BF16 || p.dtype == MTPSD_FP8_DS_MLA) {
-    const bool fp8kv = p.dtype == MTPSD_FP8_DS_MLA;
-    static std::atomic<uint64_t> attr{0}, attr8{0};
-    if (!(fp8kv ? set_smem_limit_once(sparse_mla_bf16_kernel<true>, MlaSmemT<true>::BYTES, attr8)
-                : set_smem_limit_once(sparse_mla_bf16_kernel<false>, MlaSmem::BYTES, attr))) {
+  if (p.dtype != MTPSD_F32) {
+    dim3 grid(p.R, (unsigned)ceil_div(p.H, MLA_HG), sp.n_splits);
+    static std::atomic<uint64_t> attr[3];
+    bool ok;
+    if (p.dtype == MTPSD_FP4_MLA)
+      ok = launch_portable<KV_FP4>(p, sp, grid, part_o, part_ml, st, attr[2]);
+    else if (p.dtype == MTPSD_FP8_DS_MLA)
+      ok = launch_portable<KV_FP8>(p, sp, grid, part_o, part_ml, st, attr[1]);
+    else
+      ok = launch_portable<KV_BF16>(p, sp, grid, part_o, part_ml, st, attr[0]);
+    if (!ok) {
       set_error("sparse_mla_bf16: cudaFuncSetAttribute failed");
       return MTPSD_ECUDA;
     }
-    dim3 grid(p.R, (unsigned)ceil_div(p.H, MLA_HG), sp.n_splits);
-    if (fp8kv)
-      launch_k(sparse_mla_bf16_kernel<true>, grid, 256, MlaSmemT<true>::BYTES, st, p, sp, part_o, part_ml);
-    else
-      launch_k(sparse_mla_bf16_kernel<false>, grid, 256, MlaSmem::BYTES, st, p, sp, part_o, part_ml);
     int rc = check_launch("sparse_mla_bf16");
     if (rc) return rc;
     if (sp.n_splits > 1) {
