@@ -28,4 +28,12 @@ int launch_norm_rope(const NormRopePlan& p, cudaStream_t st);
 int launch_pack_latent_fp4(const void* latent, bool f32_in, int64_t T, uint8_t* out, const int64_t* slots, int64_t pool,
                            int32_t* status, cudaStream_t st);
 
+// Sparse MLA over 4-bit rows on the tensor cores: whether this call can take it, the positions per split, whether that many splits
+// of a row are merged in the kernel.
+bool mla4_tc_supported(const MlaPlan& p);
+int mla4_tc_per_split(int R, int H, int64_t total);
+bool mla4_tc_fuse(int n_splits);
+int launch_sparse_mla4_tc(const MlaPlan& p, int n_splits, int per_split, float* part_o, float* part_ml, cudaStream_t st,
+                          bool* combined);
+
 }  // namespace mtpsd

@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "cache.h"
 #include "common.cuh"
 #include "internal.h"
 #include "latent4.cuh"
@@ -565,17 +566,19 @@ static MlaSplit choose_split(int R, int H, int n_idx, int n_append, int dtype) {
   return sp;
 }
 
+static bool tc_supported(const MlaPlan& p) { return p.dtype == MTPSD_FP4_MLA ? mla4_tc_supported(p) : mla_tc_supported(p); }
 static bool use_tc(int H, int dtype) {
   MlaPlan q{};
   q.H = H; q.dtype = dtype; q.d_latent = MLA_DL; q.d_v = MLA_DV;
-  return mla_tc_supported(q);
+  return tc_supported(q);
 }
+static bool tc_fuse(int n_splits, int dtype) { return dtype == MTPSD_FP4_MLA ? mla4_tc_fuse(n_splits) : mla_tc_fuse(n_splits); }
 
 // splits of the selected list for the tensor-core kernel
-static MlaSplit plan_split_tc(int R, int H, int n_idx, int n_append) {
+static MlaSplit plan_split_tc(int R, int H, int n_idx, int n_append, int dtype) {
   int64_t total = (int64_t)n_idx + n_append;
   MlaSplit sp;
-  sp.per_split = mla_tc_per_split(R, H, total);
+  sp.per_split = dtype == MTPSD_FP4_MLA ? mla4_tc_per_split(R, H, total) : mla_tc_per_split(R, H, total);
   sp.n_splits = total > 0 ? (int)ceil_div(total, sp.per_split) : 1;
   return sp;
 }
@@ -583,7 +586,7 @@ static MlaSplit plan_split_tc(int R, int H, int n_idx, int n_append) {
 // splits of the selected list for the kernel that will run: the tensor-core kernel's own plan, or the
 // portable kernels' (at most MLA_MAX_SPLIT positions per split)
 static MlaSplit plan_split(int R, int H, int n_idx, int n_append, int dtype, bool tc) {
-  return tc ? plan_split_tc(R, H, n_idx, n_append) : choose_split(R, H, n_idx, n_append, dtype);
+  return tc ? plan_split_tc(R, H, n_idx, n_append, dtype) : choose_split(R, H, n_idx, n_append, dtype);
 }
 
 int mla_launch_count(int R, int H, int n_idx, int n_append, int dtype) {
@@ -593,7 +596,7 @@ int mla_launch_count(int R, int H, int n_idx, int n_append, int dtype) {
   if (tc && mla_tc_persist_plan(R, H, (int64_t)n_idx + n_append, dtype, &pl)) return pl.cut ? 2 : 1;
   MlaSplit sp = plan_split(R, H, n_idx, n_append, dtype, tc);
   if (sp.n_splits <= 1) return 1;
-  if (tc && mla_tc_fuse(sp.n_splits)) return 1;
+  if (tc && tc_fuse(sp.n_splits, dtype)) return 1;
   return 2;
 }
 
@@ -627,7 +630,7 @@ static bool launch_portable(const MlaPlan& p, const MlaSplit& sp, dim3 grid, flo
 int launch_sparse_mla(const MlaPlan& p, cudaStream_t st) {
   if (p.R == 0) return MTPSD_OK;
   // the kernel is decided once, and the split plan is that kernel's
-  const bool tc = mla_tc_supported(p);
+  const bool tc = tc_supported(p);
   MlaPersist pl;
   if (tc && mla_tc_persist_plan(p.R, p.H, (int64_t)p.n_idx + p.n_append, p.dtype, &pl)) {
     const size_t need = mla_tc_persist_bytes(pl);
@@ -649,9 +652,11 @@ int launch_sparse_mla(const MlaPlan& p, cudaStream_t st) {
     part_o = (float*)p.ws;
     part_ml = part_o + (size_t)p.R * p.H * sp.n_splits * MLA_DV;
   }
-  if (tc) {   // bf16 or the FP8 latent rows (dequantized by the producers)
+  if (tc) {   // bf16 or packed latent rows (dequantized by the producers)
     bool combined = false;
-    int rc = launch_sparse_mla_tc(p, sp.n_splits, (int)sp.per_split, part_o, part_ml, st, &combined);
+    int rc = p.dtype == MTPSD_FP4_MLA
+                 ? launch_sparse_mla4_tc(p, sp.n_splits, (int)sp.per_split, part_o, part_ml, st, &combined)
+                 : launch_sparse_mla_tc(p, sp.n_splits, (int)sp.per_split, part_o, part_ml, st, &combined);
     if (rc) return rc;
     if (sp.n_splits > 1 && !combined) {
       return launch_combine<__nv_bfloat16>(p, sp.n_splits, mla_tc_ml_halves(), part_o, part_ml, st);
