@@ -46,34 +46,32 @@ namespace m4 {
 
 constexpr int DL = 576, DV = 512, DVH = 256;
 constexpr int HG = 128;                  // heads per CTA (MMA M)
-constexpr int NT = 32, NP = 64;          // positions per gathered tile and per pair
-constexpr int NPAIR = 3, NSTAGE = 2 * NPAIR;
-constexpr int FD = 4;                    // gathered tiles in flight per producer warp
+constexpr int NP = 64;                   // positions per MMA step (a pair of TMA-sized halves: one "pair" below)
+constexpr int NPAIR = 3;                 // pair buffers in the ring
 constexpr int CHUNK = NP * 128;          // 64 dims of a pair buffer
 constexpr int PAIR_STRIDE = 5 * CHUNK;
 constexpr int XHALF = HG * 64, XSLOT = 2 * XHALF;
-constexpr int F_SCL = 2 * 512;           // staging tile: codes [2 groups][4 rows][128 B], then scales [2][4][16 B at 128 B]
-constexpr int F_TILE = F_SCL + 2 * 128;
 constexpr int OFF_QR = 0;
 constexpr int OFF_C = OFF_QR + HG * 128;
 constexpr int OFF_X = OFF_C + NPAIR * PAIR_STRIDE;
 constexpr int OFF_STG = OFF_X + 2 * XSLOT;
+constexpr int NT = 32, FD = 4;           // positions per gathered tile, gathered tiles in flight
+constexpr int F_SCL = NT * 128;          // staging tile: codes [32 rows][128 B], then scales [8 groups of 4 rows][16 B, at 128 B]
+constexpr int F_TILE = F_SCL + 8 * 128;
 constexpr int OFF_F = OFF_STG + 2 * XSLOT;
-constexpr int OFF_REC = OFF_F + 4 * FD * F_TILE;      // [producer][FD]: the tile's 8 pool rows, its validity bits
-constexpr int REC = 48;
-constexpr int OFF_MASK = OFF_REC + 4 * FD * REC;      // [NSTAGE][4]
-constexpr int OFF_MREF = OFF_MASK + NSTAGE * 16;      // [128] reference maxima
+constexpr int OFF_MASK = OFF_F + FD * F_TILE;         // [NPAIR] 64 validity bits
+constexpr int OFF_MREF = OFF_MASK + 32;               // [128] reference maxima
 constexpr int OFF_ML = OFF_MREF + HG * 4;             // [2][128] (reference, sum) of the warpgroups
 constexpr int OFF_BAR = OFF_ML + 2 * HG * 8;
-constexpr int B_CFULL = 0, B_CEMPTY = B_CFULL + NSTAGE, B_SFULL = B_CEMPTY + NPAIR, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
-              B_XFULL = B_PVDONE + 2, B_XFREE = B_XFULL + 4, B_DEC = B_XFREE + 2, B_FFULL = B_DEC + 8, B_QREADY = B_FFULL + 4 * FD,
-              B_DRAIN = B_QREADY + 1, N_BARS = B_DRAIN + 1;
+constexpr int B_CFULL = 0, B_CEMPTY = B_CFULL + NPAIR, B_SFULL = B_CEMPTY + NPAIR, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
+              B_XFULL = B_PVDONE + 2, B_XFREE = B_XFULL + 4, B_DEC = B_XFREE + 2, B_FFULL = B_DEC + 8, B_FEMPTY = B_FFULL + FD, B_QREADY = B_FEMPTY + FD, B_DRAIN = B_QREADY + 1,
+              N_BARS = B_DRAIN + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;      // and room to align
-static_assert(SMEM_BYTES <= 232448 && OFF_F % 1024 == 0 && OFF_C % 1024 == 0 && OFF_REC % 16 == 0 && OFF_BAR % 8 == 0, "shared memory");
+static_assert(SMEM_BYTES <= 232448 && OFF_C % 1024 == 0 && OFF_BAR % 8 == 0, "shared memory");
 static_assert(4 * 8 * 4096 <= OFF_STG - OFF_C, "the float32 output boxes lie in the drained ring and receive slots");
-constexpr int THREADS = 416;
-constexpr int PROD_WARP = 8, N_PROD = 4, MMA_WARP = 12;
+constexpr int DEQ_WARP = 8, N_DEQ = 4, GATHER_WARP = DEQ_WARP + N_DEQ, N_GATHER = 2, MMA_WARP = GATHER_WARP + N_GATHER;
+constexpr int THREADS = 32 * (MMA_WARP + 1);
 constexpr int TM_Q = 0, TM_S0 = 128, TM_O = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
@@ -86,6 +84,7 @@ struct Params {
   float sl2;                  // softmax scale * log2(e) * 2^14
   int64_t row_pos_add;
   const __nv_bfloat16* q;
+  const uint8_t* latent;
   int64_t pool;
   const int64_t* cache_start;
   const int32_t* bt;          // block table of a paged cache, or null
@@ -113,9 +112,6 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ void bar_arrive_tx(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {   // no arrival
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
-}
 // Relaxed: what it releases has been read into registers already.
 __device__ __forceinline__ void bar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
@@ -128,6 +124,9 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
   asm volatile("{\n .reg .b32 rx;\n .reg .pred px;\n elect.sync rx|px, 0xffffffff;\n selp.b32 %0, 1, 0, px;\n}\n" : "=r"(pred));
   return pred != 0;
+}
+__device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {   // no arrival
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int* y, uint64_t* bar) {
   asm volatile(
@@ -287,11 +286,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = (uint64_t*)(sm + OFF_BAR);
   uint64_t *c_full = bars + B_CFULL, *c_empty = bars + B_CEMPTY, *s_full = bars + B_SFULL, *p_full = bars + B_PFULL,
            *pv_done = bars + B_PVDONE, *x_full = bars + B_XFULL, *x_free = bars + B_XFREE, *dec = bars + B_DEC,
-           *f_full = bars + B_FFULL, *q_ready = bars + B_QREADY, *drain = bars + B_DRAIN;
+           *f_full = bars + B_FFULL, *f_empty = bars + B_FEMPTY, *q_ready = bars + B_QREADY, *drain = bars + B_DRAIN;
   uint32_t* tmem_slot = (uint32_t*)(sm + OFF_MISC);
   volatile int* abort_flag = (volatile int*)(sm + OFF_MISC + 4);
   volatile int* given_up = (volatile int*)(sm + OFF_MISC + 8);   // some CTA of the cluster has aborted
-  uint32_t* mask_s = (uint32_t*)(sm + OFF_MASK);
+  uint8_t* mask_s = sm + OFF_MASK;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t crank;                          // value half + 2 * split of the cluster
@@ -303,10 +302,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int n_pairs = j1 > j0 ? (int)((j1 - j0 + NP - 1) / NP) : 0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NSTAGE; ++i) bar_init(&c_full[i], N_PROD);
-    for (int i = 0; i < NPAIR; ++i) bar_init(&c_empty[i], 1);
+    for (int i = 0; i < NPAIR; ++i) {
+      bar_init(&c_full[i], N_DEQ + N_GATHER);
+      bar_init(&c_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&s_full[i], 1);
+      bar_init(&s_full[i], 2);             // the MMAs' commit, and the MMA warp (it hands on the validity bits)
       bar_init(&p_full[i], 4);             // one arrival per warp
       bar_init(&pv_done[i], 1);
       bar_init(&x_full[2 * i], 1);
@@ -314,7 +315,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       bar_init(&x_free[i], 4);             // one arrival per warp of the other CTA's warpgroup
     }
     for (int i = 0; i < 8; ++i) bar_init(&dec[i], 1);
-    for (int i = 0; i < 4 * FD; ++i) bar_init(&f_full[i], 1);
+    for (int i = 0; i < FD; ++i) {
+      bar_init(&f_full[i], N_GATHER);
+      bar_init(&f_empty[i], N_DEQ);
+    }
     bar_init(q_ready, 8);                  // one arrival per warp
     bar_init(drain, 1);
     *abort_flag = 0;
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (warp == PROD_WARP && lane == 0) {
+  if (warp == GATHER_WARP && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tm_codes) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tm_scale) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tm_rope) : "memory");
@@ -393,9 +397,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         bar_arrive_tx(&x_full[2 * w], XHALF);
         bar_arrive_tx(&x_full[2 * w + 1], XHALF);
       }
-      ok = wait_all(&s_full[w], par, abort_flag, p.status);
       // the other CTA has taken pair P - 2 out of its slot: slot and staging may be written again
-      if (ok && P >= 2) ok = wait_all<true>(&x_free[w], ((P - 2) >> 1) & 1, abort_flag, p.status);
+      if (P >= 2) ok = wait_all<true>(&x_free[w], ((P - 2) >> 1) & 1, abort_flag, p.status);
+      ok = ok && wait_all(&s_full[w], par, abort_flag, p.status);
       if (!ok) break;
       fence_after();
       uint32_t sr[64];
@@ -420,14 +424,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                   x_peer + half * XHALF), "r"(stg_warp + half * XHALF), "r"(2048), "r"(xfull_peer + half * 8)
               : "memory");
       }
-      // validity of the pair's positions (written by the producers before they released its tiles)
-      const int st0 = 2 * (P % NPAIR);
-      const uint32_t cpar = (P / NPAIR) & 1;
-      ok = wait_all(&c_full[st0], cpar, abort_flag, p.status);
-      ok = ok && wait_all(&c_full[st0 + 1], cpar, abort_flag, p.status);
-      if (!ok) break;
-      const uint4 k0 = *(const uint4*)(mask_s + st0 * 4), k1 = *(const uint4*)(mask_s + st0 * 4 + 4);
-      const uint32_t mk[2] = {k0.x | k0.y | k0.z | k0.w, k1.x | k1.y | k1.z | k1.w};
+      const uint2 mk2 = *(const uint2*)(mask_s + 8 * (P % NPAIR));
+      const uint32_t mk[2] = {mk2.x, mk2.y};
+      // the head's reference as pair P - 1 left it (while the other CTA's scores are on their way)
+      float m_old = -INFINITY;
+      if (P > 0) {
+        ok = wait_all(&dec[4 * (w ^ 1) + quad], ((P - 1) >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        m_old = mref[h];
+      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -457,13 +462,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) bar_arrive_remote(xfree_peer);
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // the head's reference as pair P - 1 left it
-      float m_old = -INFINITY;
-      if (P > 0) {
-        ok = wait_all(&dec[4 * (w ^ 1) + quad], ((P - 1) >> 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        m_old = mref[h];
-      }
       const bool grow = mt > m_old + RESCALE_LOG2 || (m_old == -INFINITY && mt > -INFINITY);
       const float m_new = grow ? mt : m_old;
       mref[h] = m_new;
@@ -602,16 +600,72 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok && head_ok && w == 0)   // each value half carries its own (max, sum)
         *(float2*)(p.part_ml + ((rh * p.n_splits + split) * 2 + rank) * 2) = make_float2(l > 0.f ? m_fin : -INFINITY, l);
     }
-  } else if (warp < PROD_WARP + N_PROD) {
-    // ------------------------------------------------ producers
-    // Warp pw takes the 4-row groups pw and pw + 4 of every tile: positions 4 pw + i (i < 4) and 16 + 4 pw + i - 4.  The entries of
-    // BT = 4 tiles are looked up at once, one per lane (lane = 8 * tile + i): loaded two blocks ahead, their pages one.
-    constexpr int BT = 4;
-    const int pw = warp - PROD_WARP;
-    const int my_pos = 4 * pw + (lane & 3) + 4 * (lane & 4);       // within tile lane / 8 of a block
+  } else if (warp < DEQ_WARP + N_DEQ) {
+    // ------------------------------------------------ dequantization: rows 8 dw .. 8 dw + 7 of each tile
+    // Eight lanes a row, each with 16 bytes of codes (32 values) and their two scales.
+    const int dw = warp - DEQ_WARP, j = lane & 7, sub = lane >> 3;
+    // Word m of a lane's four goes out in turn (m + j / 2) mod 4, so that the eight lanes of a row write to all banks.
+    const int rot = j >> 1;
+    const bool r1 = rot & 1, r2 = rot & 2;
+    uint32_t dst[4];                       // byte offsets for row 8 dw + sub; 4 rows further: 512 on, bit 6 of the piece flipped
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      dst[m] = (uint32_t)(j >> 1) * CHUNK + (8 * dw + sub) * 128 + (((4 * (j & 1) + ((m + rot) & 3)) ^ sub) << 4);
+    const uint32_t src_code = saddr(sm + OFF_F) + (8 * dw + sub) * 128 + 16 * j;
+    const uint32_t src_scale = saddr(sm + OFF_F) + F_SCL + 2 * dw * 128 + sub * 16 + 2 * j;
+    for (int P = 0; P < n_pairs; ++P) {
+      const int q = P % NPAIR, n = P / NPAIR, f0 = (2 * P) % FD;
+      const uint32_t fpar = ((2 * P) / FD) & 1;
+      uint4 cd[4];
+      uint32_t scl[4];
+      bool ok = wait_all(&f_full[f0], fpar, abort_flag, p.status) && wait_all(&f_full[f0 + 1], fpar, abort_flag, p.status);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {        // tile i / 2, rows + 4 (i % 2)
+        const uint32_t at = (uint32_t)(f0 + (i >> 1)) * F_TILE;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(cd[i].x), "=r"(cd[i].y), "=r"(cd[i].z), "=r"(cd[i].w)
+                     : "r"(src_code + at + (i & 1) * 512) : "memory");
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src_scale + at + (i & 1) * 128) : "memory");
+        scl[i] = v;
+      }
+      if (n > 0 && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) break;
+      const uint32_t pair = saddr(sm + OFF_C + q * PAIR_STRIDE);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 c = cd[i];
+        const uint32_t a0 = r1 ? c.y : c.x, a1 = r1 ? c.z : c.y, a2 = r1 ? c.w : c.z, a3 = r1 ? c.x : c.w;
+        const uint32_t wd[4] = {r2 ? a2 : a0, r2 ? a3 : a1, r2 ? a0 : a2, r2 ? a1 : a3};
+        uint32_t sc[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t code = (scl[i] >> (8 * k)) & 255u;
+          const uint32_t v = code * 0x00100010u + 0x6f806f80u;   // bf16 of the scale * 2^112, twice: (code + 8 * 223) << 4
+          sc[k] = code == 0 ? 0u : (code == 255 ? 0x7fff7fffu : v);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t s = ((m + rot) & 2) ? sc[1] : sc[0];
+          sts128(pair + ((dst[m] + (i >> 1) * (NT * 128) + (i & 1) * 512) ^ ((i & 1) * 64)), mul_bf16x2(lat4::pair_bits<0>(wd[m]), s),
+                 mul_bf16x2(lat4::pair_bits<1>(wd[m]), s), mul_bf16x2(lat4::pair_bits<2>(wd[m]), s),
+                 mul_bf16x2(lat4::pair_bits<3>(wd[m]), s));
+        }
+      }
+      fence_async();                       // the MMAs read these stores; the next gathers overwrite what was read
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(&c_full[q]);
+        bar_arrive(&f_empty[f0]);
+        bar_arrive(&f_empty[f0 + 1]);
+      }
+    }
+  } else if (warp < MMA_WARP) {
+    // ------------------------------------------------ gathers: positions 16 gw .. 16 gw + 15 of each tile
+    // Two tiles' entries are looked up at once, one per lane (lane = 16 * tile + position): loaded two blocks ahead, their pages one.
+    const int gw = warp - GATHER_WARP;
     const int n_tiles = 2 * n_pairs;       // a last half pair is filled with rows outside the map: zeros
     const int32_t* idx_row = p.idx + (int64_t)r * p.n_idx;
-    auto place = [&](int blk) -> int64_t { return j0 + (int64_t)(blk * BT + (lane >> 3)) * NT + my_pos; };
+    auto place = [&](int blk) -> int64_t { return j0 + (int64_t)(2 * blk + (lane >> 4)) * NT + 16 * gw + (lane & 15); };
     auto raw = [&](int blk) -> int32_t { return p.n_idx > 0 ? idx_row[min(place(blk), (int64_t)p.n_idx - 1)] : 0; };
     int32_t e0 = raw(0), e1 = raw(1), e2 = raw(2);       // (clamped: any block may be asked for)
     const int64_t limit = p.row_pos[r] + p.row_pos_add;
@@ -619,103 +673,67 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int breq = request_of_row_warp(p.row_offsets, p.B, (uint32_t)r);
     const int64_t base = PAGED ? 0 : p.cache_start[breq];
     auto pos_of = [&](int blk, int32_t e) -> int64_t {
-      const int64_t j = place(blk);
-      if (j >= j1) return -1;
-      return entry_pos(p, j < p.n_idx ? (int64_t)e : abase + (j - p.n_idx), limit);
+      const int64_t at = place(blk);
+      if (at >= j1) return -1;
+      return entry_pos(p, at < p.n_idx ? (int64_t)e : abase + (at - p.n_idx), limit);
     };
     int64_t s1 = pos_of(0, e0);            // positions and pages of the next block
     int32_t pg1 = PAGED ? page_entry(p, breq, s1) : -1;
-    int32_t row = 0;                       // pool rows of the present block (a row outside the map reads zeros), which of them are there
-    uint32_t there = 0;
-    uint8_t* const fstg = sm + OFF_F + pw * FD * F_TILE;
-    uint8_t* const rec = sm + OFF_REC + pw * FD * REC;
-    uint64_t* const ff = f_full + pw * FD;
-    // rope values of a tile straight into their chunk of the pair buffer (rank 0); y: the 8 pool rows
-    auto issue_rope = [&](int t, const int* y) {
-      bar_expect_tx(&c_full[t % NSTAGE], 1024);
-      const uint32_t dst = saddr(sm + OFF_C + ((t >> 1) % NPAIR) * PAIR_STRIDE + 4 * CHUNK) + (t & 1) * (NT * 128) + pw * 512;
-      gather4(dst, &tm_rope, 0, y, &c_full[t % NSTAGE]);
-      gather4(dst + 4 * 512, &tm_rope, 0, y + 4, &c_full[t % NSTAGE]);
-    };
-    auto issue_tile = [&](int t) {
-      if (t % BT == 0) {                   // the next block becomes the present one
-        const int blk = t / BT;
+    int32_t row = 0;                       // pool rows of the present block (a row outside the map reads zeros)
+    uint32_t there = 0;                    // which of them are there
+    int done = 0;                          // tiles whose gathers have been issued
+    for (int t = 0; t < n_tiles; ++t) {
+      if (t % 2 == 0) {                    // the next block becomes the present one
+        const int blk = t / 2;
         const int64_t rw = entry_row<PAGED>(p, s1, base, pg1);
         row = rw >= 0 ? (int32_t)rw : (int32_t)p.pool;
         there = __ballot_sync(0xffffffffu, rw >= 0);
+        if (rank == 0 && rw >= 0) {        // the rope values are fetched a little later
+          const uint8_t* rope = p.latent + rw * lat4::ROW + lat4::OFF_ROPE;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(rope));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(rope + 127));
+        }
         s1 = pos_of(blk + 1, e1);
         if (PAGED) pg1 = page_entry(p, breq, s1);
         e1 = e2;
         e2 = raw(blk + 3);
       }
-      const int k = t % FD;
-      int y[8];
+      int y[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, row, (t % BT) * 8 + i);
-      const uint32_t v = there >> ((t % BT) * 8);
-      if ((lane >> 3) == t % BT) *(int*)(rec + k * REC + 4 * (lane & 7)) = row;
-      if (lane == 0) *(uint32_t*)(rec + k * REC + 32) = (v & 15u) << (4 * pw) | ((v >> 4) & 15u) << (16 + 4 * pw);
-      __syncwarp();
-      const uint32_t dst = saddr(fstg + k * F_TILE);
+      for (int i = 0; i < 16; ++i) y[i] = __shfl_sync(0xffffffffu, row, 16 * (t & 1) + i);
+      const int f = t % FD, P = t >> 1, q = P % NPAIR, n = P / NPAIR;
+      if (t >= FD && !wait_all(&f_empty[f], (t / FD - 1) & 1, abort_flag, p.status)) break;
+      const uint32_t dst = saddr(sm + OFF_F + f * F_TILE);
       if (elect_one()) {
-        bar_arrive_tx(&ff[k], 2 * (512 + 64));
+        bar_arrive_tx(&f_full[f], 16 * (128 + 16));
 #pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          gather4(dst + gi * 512, &tm_codes, (int)rank * 128, y + 4 * gi, &ff[k]);
-          gather4(dst + F_SCL + gi * 128, &tm_scale, lat4::OFF_SCALE + (int)rank * 16, y + 4 * gi, &ff[k]);
+        for (int g = 0; g < 4; ++g) {
+          gather4(dst + (4 * gw + g) * 512, &tm_codes, (int)rank * 128, y + 4 * g, &f_full[f]);
+          gather4(dst + F_SCL + (4 * gw + g) * 128, &tm_scale, lat4::OFF_SCALE + (int)rank * 16, y + 4 * g, &f_full[f]);
         }
-        if (rank == 0 && (t >> 1) < NPAIR) issue_rope(t, y);   // the first pairs' buffers are free
-      }
-      __syncwarp();
-    };
-    // dequantization: lane = word of a row's 256 dims here, i.e. chunk lane / 8, 16-byte piece lane % 8
-    const uint32_t piece = (uint32_t)(lane >> 3) * CHUNK;
-    int ti = 0, done = 0;
-    bool ok = true;
-    for (int t = 0; t < n_tiles && ok; ++t) {
-      while (ti < n_tiles && ti < t + FD) issue_tile(ti++);
-      const int k = t % FD, st = t % NSTAGE, P = t >> 1, q = P % NPAIR, n = P / NPAIR;
-      if (n > 0) {
-        ok = wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        if (rank == 0) {
-          if (elect_one()) {
-            const int4 a = *(const int4*)(rec + k * REC), b = *(const int4*)(rec + k * REC + 16);
-            const int y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            issue_rope(t, y);
-          }
-          __syncwarp();
-        }
-      }
-      ok = wait_all(&ff[k], (t / FD) & 1, abort_flag, p.status);
-      if (!ok) break;
-      const uint8_t* src = fstg + k * F_TILE;
-      uint8_t* pair = sm + OFF_C + q * PAIR_STRIDE + (t & 1) * (NT * 128) + pw * 512 + piece;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int gi = i >> 2, rg = i & 3;       // group, row of it
-        const uint32_t word = *(const uint32_t*)(src + gi * 512 + rg * 128 + lane * 4);
-        const uint32_t c = src[F_SCL + gi * 128 + rg * 16 + (lane >> 1)];
-        uint32_t sc = c * 0x00100010u + 0x6f806f80u;        // bf16 of the scale * 2^112, twice: (code + 8 * 223) << 4
-        sc = c == 0 ? 0u : (c == 255 ? 0x7fff7fffu : sc);
-        // position 16 gi + 4 pw + rg of the tile; its swizzle is by position mod 8
-        *(uint4*)(pair + gi * 2048 + rg * 128 + (((lane & 7) ^ (4 * (pw & 1) + rg)) << 4)) =
-            make_uint4(mul_bf16x2(lat4::pair_bits<0>(word), sc), mul_bf16x2(lat4::pair_bits<1>(word), sc),
-                       mul_bf16x2(lat4::pair_bits<2>(word), sc), mul_bf16x2(lat4::pair_bits<3>(word), sc));
-      }
-      fence_async();                       // the MMAs read these stores; the next gathers overwrite what was read
-      const uint32_t bits = *(const uint32_t*)(rec + k * REC + 32);
-      __syncwarp();
-      if (lane == 0) {
-        mask_s[st * 4 + pw] = bits;
-        bar_arrive(&c_full[st]);
       }
       __syncwarp();
       done = t + 1;
+      // validity bits and (rank 0) the rope values, straight into their chunk, once the pair buffer is free
+      if (n > 0 && !(t & 1) && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) break;
+      if (lane == 0) *(uint16_t*)(mask_s + 8 * q + 4 * (t & 1) + 2 * gw) = (uint16_t)(there >> (16 * (t & 1)));
+      __syncwarp();
+      if (elect_one()) {
+        if (rank == 0) {
+          if (t & 1) bar_arrive_tx(&c_full[q], 2048);
+          else bar_expect_tx(&c_full[q], 2048);
+          const uint32_t rope = saddr(sm + OFF_C + q * PAIR_STRIDE + 4 * CHUNK) + (t & 1) * (NT * 128) + gw * 2048;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) gather4(rope + g * 512, &tm_rope, 0, y + 4 * g, &c_full[q]);
+        } else if (t & 1) {
+          bar_arrive(&c_full[q]);
+        }
+      }
+      __syncwarp();
     }
     if (*abort_flag && lane == 0) {        // copies in flight land before exit (waits bounded once more)
       volatile int dummy = 0;
-      for (int t = done; t < ti; ++t) mbar::wait<false>(&ff[t % FD], (t / FD) & 1, &dummy, p.status, WAIT_NS);
+      for (int t = max(0, done - FD); t < done; ++t) mbar::wait<false>(&f_full[t % FD], (t / FD) & 1, &dummy, p.status, WAIT_NS);
     }
   } else {
     // ------------------------------------------------ MMA issue: QK(0), then for every pair P QK(P + 1) and PV(P)
@@ -728,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto qk = [&](int n) -> bool {
       const int b = n % NPAIR;
       const uint32_t par = (n / NPAIR) & 1;
-      if (!wait_all(&c_full[2 * b], par, abort_flag, p.status) || !wait_all(&c_full[2 * b + 1], par, abort_flag, p.status)) return false;
+      if (!wait_all(&c_full[b], par, abort_flag, p.status)) return false;
       fence_after();
       const uint64_t cd = c_desc0 + (uint64_t)((b * PAIR_STRIDE) >> 4);
       const uint32_t d = tmem + TM_S0 + (n & 1) * 64;
@@ -740,6 +758,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (k < 16) mma_ts(d, tmem + TM_Q + k * 8, cd + off, IDESC_QK, k > 0 ? 1u : 0u);
             else mma_ss(d, qr_desc + (uint64_t)(((k & 3) * 32) >> 4), cd + off, IDESC_QK, 1u);
           }
+        bar_arrive(&s_full[n & 1]);
         commit(&s_full[n & 1]);
       }
       __syncwarp();
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(saddr((const void*)given_up), c)), "r"(1) : "memory");
   // neither CTA starts another copy into the other's shared memory, and with fused splits every partial of the row is written
   cluster_sync();
-  if (*given_up) {     // what was sent or gathered without anyone waiting for it lands meanwhile; nothing is merged
+  if (*given_up) {     // copies in flight that nobody waits for (sent by the other CTA, gathered here) land meanwhile; nothing is merged
     const uint64_t t0 = mbar::globaltimer_ns();
     while (mbar::globaltimer_ns() - t0 < 200000) {}
     return;
@@ -876,7 +895,7 @@ int launch_sparse_mla4_tc(const MlaPlan& p, int n_splits, int per_split, float* 
   Params k;
   k.B = p.B; k.R = p.R; k.H = p.H; k.n_idx = p.n_idx; k.n_append = p.n_append;
   k.sl2 = p.scale * LOG2E * UP; k.row_pos_add = p.row_pos_add;
-  k.q = (const __nv_bfloat16*)p.q; k.pool = p.pool;
+  k.q = (const __nv_bfloat16*)p.q; k.latent = (const uint8_t*)p.latent; k.pool = p.pool;
   k.cache_start = p.cache_start; k.bt = p.pg.bt; k.bt_stride = p.pg.stride; k.pg_shift = p.pg.shift;
   k.row_offsets = p.row_offsets; k.row_pos = p.row_pos; k.idx = p.idx; k.append_base = p.append_base;
   k.out = (__nv_bfloat16*)p.out; k.lse = p.lse; k.part_o = part_o; k.part_ml = part_ml;
