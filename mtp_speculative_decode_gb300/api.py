@@ -758,7 +758,10 @@ def _opt(t, name: str, dev: int, dtype, ndim: int, numel: Optional[int] = None):
     """The address of an optional tensor (None stays None), checked like _tensor."""
     if t is None:
         return None
-    p = _tensor(t, name, dev, dtype, ndim)
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.ndim == ndim and (
+            numel is None or t.numel() == numel):
+        return t.data_ptr()
+    p = _tensor(t, name, dev, dtype, ndim)      # says what is wrong
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
     return p
@@ -855,62 +858,63 @@ def _head_side(t, name, dev, norm, weight, bias, norm_dim, rot_start, out, scale
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}, is on {t.device}")
-    if t.dtype not in _TYPES:
+    in_type = _TYPES.get(t.dtype)
+    if in_type is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() not in (2, 3):
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        T, heads, D = shape
+        x_hs = st[1]
+    elif len(shape) == 2:
+        (T, D), heads = shape, 1
+        x_hs = D
+    else:
         raise ValueError(f"{name} must be [T, heads, D] or [T, D]")
-    T, D = t.shape[0], t.shape[-1]
-    heads = t.shape[1] if t.dim() == 3 else 1
-    st = t.stride()
-    if D > 1 and t.numel() and st[-1] != 1:
+    if D > 1 and st[-1] != 1 and T and heads:
         raise ValueError(f"{name} must have contiguous heads")
-    if norm not in _NORMS:
+    kind = _NORMS.get(norm, -1)
+    if kind < 0:
         raise ValueError(f"{name}_norm must be None, 'rms' or 'layer'")
     nd = D if norm_dim is None else int(norm_dim)
-    pw = _opt(weight, f"{name}_weight", dev, torch.float32, 1, nd)
-    pb = _opt(bias, f"{name}_bias", dev, torch.float32, 1, nd)
+    pw = None if weight is None else _opt(weight, f"{name}_weight", dev, torch.float32, 1, nd)
+    pb = None if bias is None else _opt(bias, f"{name}_bias", dev, torch.float32, 1, nd)
     rows = T if pool is None else pool
     if out is None:
         if pool is not None:
             raise ValueError(f"slots need {name}_out, the cache")
-        out = _empty(stream, *t.shape, dtype=t.dtype, device=t.device)
+        out = _empty(stream, *shape, dtype=t.dtype, device=t.device)
     if not isinstance(out, torch.Tensor):
         raise TypeError(f"{name}_out must be a torch tensor")
     if out.get_device() != dev:
         raise ValueError(f"{name}_out must be a CUDA tensor on the current device cuda:{dev}, is on {out.device}")
-    so = out.stride()
-    packed = out.dtype == torch.uint8 and D == 576 and out.dim() == 2 and out.shape[1] in (656, 416)
-    if packed:
-        if out.shape[0] != rows or heads != 1:
-            raise ValueError(f"{name}_out must have {rows} cache rows, of one head")
-        dtype, hs = _latent_dtype(out), 0
-    else:
-        if out.dtype == torch.uint8:
-            dtype = N.MTPSD_FP8_E4M3
-        elif out.dtype in _TYPES:
-            dtype = _TYPES[out.dtype]
-        else:
-            raise TypeError(f"{name}_out must be bfloat16, float32 or uint8, got {out.dtype}")
-        if tuple(out.shape) != (rows, heads, D) and not (heads == 1 and tuple(out.shape) == (rows, D)):
-            raise ValueError(f"{name}_out must be [{rows}, {heads}, {D}], got {list(out.shape)}")
-        hs = so[1] if out.dim() == 3 else D
-    if out.numel() and so[-1] != 1 and out.shape[-1] > 1:
-        raise ValueError(f"{name}_out must have contiguous rows")
-    if rows > 1 and out.numel():
-        # heads inside their row, rows apart
-        if (heads > 1 and hs < D) or so[0] < (out.shape[1] if packed else D) or \
-                not (so[0] >= (heads - 1) * hs + D or packed or hs >= (rows - 1) * so[0] + D):
-            raise ValueError(f"{name}_out must have heads that do not overlap")
+    o_shape, so = out.shape, out.stride()
     psc = None
-    if dtype == N.MTPSD_FP8_E4M3:
-        if scale is None:
-            raise ValueError(f"{name}_out of codes needs {name}_scale")
-        psc = _tensor(scale, f"{name}_scale", dev, torch.float32, scale.dim())
-        if scale.numel() != rows * heads:
-            raise ValueError(f"{name}_scale must have {rows * heads} entries")
-    side = N.HeadSide(t.data_ptr(), st[0], st[1] if t.dim() == 3 else D, heads, D, _TYPES[t.dtype], _NORMS[norm], nd,
-                      int(rot_start), pw, pb, out.data_ptr(), so[0], hs, dtype, psc)
-    return side, out
+    dtype = _TYPES.get(out.dtype)
+    width = D
+    if dtype is None:
+        if out.dtype is not torch.uint8:
+            raise TypeError(f"{name}_out must be bfloat16, float32 or uint8, got {out.dtype}")
+        dtype = N.MTPSD_FP8_E4M3
+        if D == 576 and len(o_shape) == 2 and heads == 1 and o_shape[1] in (656, 416):     # cache rows
+            width = o_shape[1]
+            dtype = N.MTPSD_FP4_MLA if width == 416 else N.MTPSD_FP8_DS_MLA
+        else:
+            if scale is None:
+                raise ValueError(f"{name}_out of codes needs {name}_scale")
+            psc = _opt(scale, f"{name}_scale", dev, torch.float32, scale.dim(), rows * heads)
+    if o_shape != (rows, heads, width) and not (heads == 1 and o_shape == (rows, width)):
+        raise ValueError(f"{name}_out must be [{rows}, {heads}, {width}], got {list(o_shape)}")
+    o_ts, o_hs = so[0], so[1] if len(so) == 3 else width
+    if rows and heads:
+        if width > 1 and so[-1] != 1:
+            raise ValueError(f"{name}_out must have contiguous rows")
+        # heads side by side within a token, or tokens within a head
+        if heads > 1 and o_hs < width or rows > 1 and o_ts < width or \
+                heads > 1 and rows > 1 and o_ts < (heads - 1) * o_hs + width and o_hs < (rows - 1) * o_ts + width:
+            raise ValueError(f"{name}_out must have heads that do not overlap")
+    # in the order of the structure's fields
+    return N.HeadSide(t.data_ptr(), st[0], x_hs, heads, D, in_type, kind, nd, rot_start, pw, pb, out.data_ptr(), o_ts, o_hs, dtype,
+                      psc), out
 
 
 def norm_rope(positions, cos_sin, q=None, k=None, q_norm=None, q_weight=None, q_bias=None, q_norm_dim=None, q_rot_start=0,

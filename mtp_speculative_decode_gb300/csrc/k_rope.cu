@@ -328,8 +328,11 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
   }
 }
 
+// CTAs of 256 threads per SM that the registers have to allow: the loads in flight carry the bandwidth.  Measured on 16384 x 128
+// heads of 64 rope values (bf16): see the launch.
+constexpr int min_ctas(bool f32, int slots) { return slots >= 8 ? 1 : (slots >= 4 ? (f32 ? 2 : 3) : (f32 ? 3 : 4)); }
 template <bool F32, int QP, int QR, int KP, int KR>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(256, min_ctas(F32, 2 * (QP > KP ? QP : KP) + (QR > KR ? QR : KR))) norm_rope_kernel(const __grid_constant__ Args a) {
   griddep_wait();                // the previous kernel's writes are visible from here on
   griddep_launch_dependents();
   if ((int)blockIdx.x < a.q.blocks) run_side<F32, QP, QR>(a, a.q, blockIdx.x);
@@ -475,8 +478,10 @@ int launch_norm_rope(const NormRopePlan& p, cudaStream_t st) {
   const mtpsd_head_side* c[2] = {p.q, p.k};
   for (int i = 0; i < 2; ++i)
     if (c[i]) inst[i] = plan_side(*c[i], p, i == 1, &side[i]);
-  // both sides in one launch where both take the vector kernel on one type
-  if (inst[0] >= 0 && inst[1] >= 0 && side[0].in_f32 == side[1].in_f32) {
+  // Both sides in one launch where both take the vector kernel on one type; but a large call whose sides take different forms of it
+  // goes in two, each with as many CTAs per SM as its own registers allow.
+  const bool large = inst[0] != inst[1] && side[0].blocks + side[1].blocks > 8 * num_sms();
+  if (inst[0] >= 0 && inst[1] >= 0 && side[0].in_f32 == side[1].in_f32 && !large) {
     a.q = side[0];
     a.k = side[1];
     if (a.q.in_f32) launch_sides<true>(a, inst[0], inst[1], st);
