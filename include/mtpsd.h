@@ -570,7 +570,8 @@ int mtpsd_process_logits(const mtpsd_logits_args* args, void* stream);
  * need_0 + .. + need_b <= n_free (or need_b = 0); the first one that is not, and each later one that needs pages,
  * gets -1 for every page that it needs and is flagged MTPSD_STATUS_NO_PAGES.
  *   old_len NULL builds the tables anew: all entries of a row are written, -1 behind its pages.
- *   lengths[b] (nullable) = new_len[b] where served, else old_len[b] (0 when built anew)
+ *   lengths[b] (nullable), the tokens that request b has pages for = max(old_len[b], new_len[b]) where served, else old_len[b]
+ *   (0 for old_len when built anew): the old_len of the next call
  *   n_free_out[0] = n_free[0] - the pages handed out; free_pages is only read.
  * A length that is negative or does not fit the row (new_len > bt_stride * page_size) leaves the request as it was (an
  * empty row when built anew, lengths[b] = old_len[b]) and is flagged MTPSD_STATUS_ROW_RANGE; so is an n_free outside

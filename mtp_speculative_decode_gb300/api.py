@@ -332,7 +332,10 @@ def sparse_mla_decode(q, latent, cache_start, row_offsets, row_pos, idx, softmax
     if out is None:
         out = _empty(stream, R, H, 512, dtype=q.dtype, device=q.device)
     nbytes = sparse_mla_workspace_size(R, H, idx.shape[1], n_append, dt)
-    ws = _ws(workspace, nbytes, q.device) if nbytes else workspace
+    if nbytes and workspace is None and dt == N.MTPSD_FP4_MLA:
+        ws = _empty(stream, nbytes, dtype=torch.uint8, device=q.device)     # the call's own: calls on two streams do not share it
+    else:
+        ws = _ws(workspace, nbytes, q.device) if nbytes else workspace
     a = N.MlaArgs(B=row_offsets.numel() - 1, R=R, n_heads=H, d_latent=DL, d_v=512, n_idx=idx.shape[1],
                   n_append=n_append, dtype=dt, softmax_scale=softmax_scale, row_pos_add=row_pos_add,
                   q=q.data_ptr(), latent=latent.data_ptr(), pool_tokens=latent.shape[0],
@@ -772,7 +775,8 @@ def block_table_grow(block_table, page_size: int, new_len, free_pages, n_free, o
     """Block tables from the requests' lengths: request b of block_table [B, n] int32 gets the pages between old_len[b] and
     new_len[b] tokens (int64 [B]; without old_len the tables are built anew) off the end of free_pages [cap] int32, of which
     n_free [1] int32 are free; n_free_out (in place without it) receives what is left.  Requests that the list has too few
-    pages for get -1 (STATUS_NO_PAGES).  lengths [B] int64 receives what each request has pages for.
+    pages for get -1 (STATUS_NO_PAGES).  lengths [B] int64 (may be old_len) receives the tokens that each request has pages for, the
+    next call's old_len.
 
     With token_offsets [B+1] uint32 (request b's tokens of this step, the last of its new length), slots [T] int64 and
     positions [T] int64 (optional) receive each token's pool slot (-1: none) and position.  Returns lengths."""

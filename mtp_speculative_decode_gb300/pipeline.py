@@ -52,12 +52,16 @@ class DecodeStep:
     step of the next round (seed_dsa_topk_from_draft_extend)."""
 
     def __init__(self, w: W.Workload, device="cuda", draft: Optional[Dict[str, torch.Tensor]] = None,
-                 seeded: bool = False, latent_fp8: bool = False, page_size: Optional[int] = None):
+                 seeded: bool = False, latent_fp8: bool = False, page_size: Optional[int] = None,
+                 latent_fp4: bool = False):
         self.w = w
         self.seeded = seeded
         self.page_size = page_size     # paged caches: every pool reached through one shared block table
         self.paged = None
+        if latent_fp8 and latent_fp4:
+            raise ValueError("the latent caches are held in 8 or in 4 bits")
         self.latent_fp8 = latent_fp8   # latent caches as 656-byte FP8 rows ([P2] "草稿层 KV 的账")
+        self.latent_fp4 = latent_fp4   # latent caches as 416-byte 4-bit rows
         spec = w.spec
         self.spec = spec
         self.device = device
@@ -104,7 +108,7 @@ class DecodeStep:
             self.q_idx, self.q_scale = self.q_idx_raw, None
         self.topk_idx = torch.empty(R, spec.topk, dtype=torch.int32, device=device)
         self.out = torch.empty(R, spec.H_Q, 512, dtype=self.q_mla.dtype, device=device)
-        mla_dt = N.MTPSD_FP8_DS_MLA if latent_fp8 else (1 if self.fp8 else 0)
+        mla_dt = N.MTPSD_FP4_MLA if latent_fp4 else N.MTPSD_FP8_DS_MLA if latent_fp8 else (1 if self.fp8 else 0)
         self.mla_dtype = mla_dt
         self.lse = torch.empty(R, spec.H_Q, dtype=torch.float32, device=device)
         self.num_accepted = torch.empty(B, dtype=torch.int32, device=device)
@@ -138,7 +142,7 @@ class DecodeStep:
                 self.src_idxs = None
             src = _gen(d, "src_latent", device)
             self.src_latent = self._latent(src.reshape(-1, 576)).reshape(src.shape[0], src.shape[1], -1) \
-                if latent_fp8 else src
+                if latent_fp8 or latent_fp4 else src
             self.dst_pos = _dev(w.L, device, torch.int64)    # accepted segment starts at L_b
             self.next_pos = torch.empty(B, dtype=torch.int64, device=device)
             self.d_q_idx_raw = _gen(d, "d_q_idx", device)
@@ -224,7 +228,9 @@ class DecodeStep:
         self.accept_index = _dev(np.tile(np.arange(Wn, dtype=np.int32), (B, 1)), device, torch.int32)
 
     def _latent(self, x):
-        """A latent pool as the step stores it: as generated, or packed into FP8 rows."""
+        """A latent pool as the step stores it: as generated, or packed into FP8 or 4-bit rows."""
+        if self.latent_fp4:
+            return api.pack_latent_fp4(x)
         return api.pack_latent_fp8(x) if self.latent_fp8 else x
 
     def _init_extend(self, d, device):
@@ -621,3 +627,68 @@ class VerifyHead:
 
     def launches_per_step(self) -> int:
         return 4 + (self.counts is not None)
+
+
+class PagedAttention:
+    """The DSA layer over paged caches, from the projections of a step's tokens to the attention's output: pages for the new
+    tokens, their slots, norms and rotation straight into the caches (FP8 indexer keys with their scales; latent rows in bf16, 8 or
+    4 bits), the indexer's selection and the sparse attention.  Any ragged step: prompt chunks, verify windows, single tokens.
+
+    B requests of at most max_len tokens share n_pages pages; H query heads and H_I indexer heads; at most max_tokens tokens a
+    step.  The weights are those of the indexer's key norm (128, with its bias) and of the latent's norm (512); cos_sin [n_pos, 64] turns the
+    first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'."""
+
+    def __init__(self, B: int, max_len: int, n_pages: int, page_size: int, cos_sin, k_weight, k_bias, latent_weight, H: int = 128,
+                 H_I: int = 64, topk: int = 2048, max_tokens: int = 4096, row_bytes: int = 416, interleaved: bool = True,
+                 eps: float = 1e-6):
+        device = cos_sin.device
+        self.B, self.page_size, self.topk, self.max_len = B, page_size, topk, max_len
+        self.cos_sin, self.k_weight, self.k_bias, self.latent_weight = cos_sin, k_weight, k_bias, latent_weight
+        self.interleaved, self.eps = interleaved, eps
+        new = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype, device=device)  # noqa: E731
+        pool = n_pages * page_size
+        self.block_table = torch.full((B, -(-max_len // page_size)), -1, dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        self.lengths = new(B, dtype=torch.int64)                # tokens that each request has pages for
+        self.k_cache, self.k_scale = new(pool, 128, dtype=torch.uint8), new(pool, dtype=torch.float32)
+        if row_bytes not in (1152, 656, 416):
+            raise ValueError("latent rows have 1152 (bf16), 656 (FP8) or 416 (4-bit) bytes")
+        self.latent = new(pool, 576, dtype=torch.bfloat16) if row_bytes == 1152 else new(pool, row_bytes, dtype=torch.uint8)
+        T = max_tokens
+        self.slots, self.positions = new(T, dtype=torch.int64), new(T, dtype=torch.int64)
+        self.q_idx, self.q_scale = new(T, H_I, 128, dtype=torch.uint8), new(T, H_I, dtype=torch.float32)
+        self.topk_idx = new(T, topk, dtype=torch.int32)
+        self.out = new(T, H, 512, dtype=torch.bfloat16)
+        self.status = new(1, dtype=torch.int32)
+
+    def step(self, new_len, token_offsets, q_idx, k_idx, w_idx, q, kv, stream=None):
+        """new_len [B] int64 (lengths after the step), token_offsets [B+1] uint32; of the step's T tokens: q_idx [T, H_I, 128], k_idx
+        [T, 128], w_idx [T, H_I] float32, q [T, H, 576] bf16 (its last 64 dims are turned in place), kv [T, 576].  Returns the
+        attention's output [T, H, 512]."""
+        T = q.shape[0]
+        slots, pos = self.slots[:T], self.positions[:T]
+        api.block_table_grow(self.block_table, self.page_size, new_len, self.free_pages, self.n_free, old_len=self.lengths,
+                             lengths=self.lengths, token_offsets=token_offsets, slots=slots, positions=pos, dev_status=self.status,
+                             stream=stream)
+        api.norm_rope(pos, self.cos_sin, q=q_idx, q_out=self.q_idx[:T], q_scale=self.q_scale[:T], k=k_idx, k_norm="layer",
+                      k_weight=self.k_weight, k_bias=self.k_bias, k_out=self.k_cache, k_scale=self.k_scale, slots=slots, eps=self.eps,
+                      dev_status=self.status, stream=stream)
+        rope = q[:, :, 512:]
+        api.norm_rope(pos, self.cos_sin, q=rope, q_out=rope, k=kv, k_norm="rms", k_weight=self.latent_weight, k_norm_dim=512,
+                      k_rot_start=512, k_out=self.latent, slots=slots, interleaved=self.interleaved, eps=self.eps,
+                      dev_status=self.status, stream=stream)
+        paged = (self.block_table, self.page_size)
+        api.indexer_topk(self.q_idx[:T], self.q_scale[:T], w_idx, self.k_cache, self.k_scale, None, token_offsets, pos, self.topk,
+                         self.max_len, topk_idx=self.topk_idx[:T], dev_status=self.status, stream=stream, paged=paged)
+        return api.sparse_mla_decode(q, self.latent, None, token_offsets, pos, self.topk_idx[:T], W.SOFTMAX_SCALE, out=self.out[:T],
+                                     dev_status=self.status, stream=stream, paged=paged)
+
+    def release(self, keep_len=None):
+        """Returns the pages behind keep_len [B] tokens (all of them without it) of every request, on the current stream."""
+        api.block_table_release(self.block_table, self.page_size, self.lengths, self.free_pages, self.n_free, keep_len=keep_len,
+                                dev_status=self.status)
+        if keep_len is None:
+            self.lengths.zero_()
+        else:
+            torch.minimum(self.lengths, keep_len, out=self.lengths)

@@ -42,7 +42,7 @@ def grow(table, page_size, new_len, free_pages, n_free, old_len=None):
             status |= NO_PAGES
             out[b, first:last] = -1
             continue
-        lengths[b] = new
+        lengths[b] = max(old, new)      # a shorter request keeps its pages
         for p in range(first, first + need):
             left -= 1
             out[b, p] = free_pages[left]

@@ -22,7 +22,7 @@ def test_grow_worked_example():
     # two pages free: the first request takes one, the second is not served, the third needs none
     out, lengths, left, st = tables.grow(t, 4, [9, 8, 3], free, 2, [5, 0, 4])
     assert out.tolist() == [[1, 2, 11, -1], [-1] * 4, [3, -1, -1, -1]]
-    assert lengths.tolist() == [9, 0, 3] and left == 1 and st == tables.NO_PAGES
+    assert lengths.tolist() == [9, 0, 4] and left == 1 and st == tables.NO_PAGES
     # built anew; a length past the row
     out, lengths, left, st = tables.grow(t, 4, [1, 17, 16], free, 6)
     assert out.tolist() == [[15, -1, -1, -1], [-1] * 4, [14, 13, 12, 11]]
