@@ -104,6 +104,11 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float n) {
   x = p * c - q * n;
   y = p * n + q * c;
 }
+// x r w with one rounding (and 2^-48): the first product's error goes into the second.
+__device__ __forceinline__ float mul3(float x, float r, float w) {
+  const float p = x * r;
+  return fmaf(p, w, fmaf(x, r, -p) * w);
+}
 // Largest over `lanes` neighbouring lanes (all lanes of the warp take part)
 __device__ __forceinline__ float group_max(float m, int lanes) {
   for (int o = lanes >> 1; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -243,7 +248,7 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
           if (s.w) {
             load8f(s.w + vec[i] * 8, wt);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * r * wt[e];
+            for (int e = 0; e < 8; ++e) v[i][e] = mul3(v[i][e], r, wt[e]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] *= r;
@@ -329,7 +334,7 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
 }
 
 // CTAs of 256 threads per SM that the registers have to allow: the loads in flight carry the bandwidth.  Measured on 16384 x 128
-// heads of 64 rope values (bf16): see the launch.
+// heads of 64 rope values (bf16): four CTAs (64 registers) take 126 us, three 133, five 155 (spills).
 constexpr int min_ctas(bool f32, int slots) { return slots >= 8 ? 1 : (slots >= 4 ? (f32 ? 2 : 3) : (f32 ? 3 : 4)); }
 template <bool F32, int QP, int QR, int KP, int KR>
 __global__ void __launch_bounds__(256, min_ctas(F32, 2 * (QP > KP ? QP : KP) + (QR > KR ? QR : KR))) norm_rope_kernel(const __grid_constant__ Args a) {
@@ -377,8 +382,7 @@ __global__ void __launch_bounds__(256) norm_rope_elements_kernel(const __grid_co
       }
       const float r = __frsqrt_rn(group_sum(sq, 32) / n + a.eps);
       for (int i = lane; i < s.norm_dim; i += 32) {
-        float y = (v[i] - mean) * r;
-        if (s.w) y *= s.w[i];
+        float y = s.w ? mul3(v[i] - mean, r, s.w[i]) : (v[i] - mean) * r;
         if (s.b) y += s.b[i];
         v[i] = y;
       }
@@ -413,8 +417,9 @@ bool fits16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Lanes and slots for the vector kernel: 0 (one pair slot), 1 (one and two rest slots), 2 (two and four); -1: the element kernel.
 int plan_side(const mtpsd_head_side& c, const NormRopePlan& p, bool key, Side* s) {
-  s->x = c.x; s->xt = c.x_token_stride; s->xh = c.x_head_stride;
-  s->out = c.out; s->ot = c.out_token_stride; s->oh = c.out_head_stride; s->scale = c.scale;
+  // (the head stride of a single head says nothing)
+  s->x = c.x; s->xt = c.x_token_stride; s->xh = c.heads > 1 ? c.x_head_stride : 0;
+  s->out = c.out; s->ot = c.out_token_stride; s->oh = c.heads > 1 ? c.out_head_stride : 0; s->scale = c.scale;
   s->w = c.weight; s->b = c.bias;
   s->slots = key ? p.slots : nullptr;
   s->pool = p.pool;
@@ -426,9 +431,9 @@ int plan_side(const mtpsd_head_side& c, const NormRopePlan& p, bool key, Side* s
   const int in_vec = s->in_f32 ? 4 : 8;                                              // elements of 16 bytes
   const int out_vec = c.out_dtype == MTPSD_F32 ? 4 : (c.out_dtype == MTPSD_BF16 ? 8 : (rows ? 16 : 8));
   const bool ok = c.D % 8 == 0 && p.rot_dim % 16 == 0 && (!p.rot_dim || c.rot_start % 8 == 0) && (!c.norm || c.norm_dim % 8 == 0) &&
-                  fits16(c.x) && c.x_token_stride % in_vec == 0 && c.x_head_stride % in_vec == 0 &&
+                  fits16(c.x) && c.x_token_stride % in_vec == 0 && s->xh % in_vec == 0 &&
                   ((uintptr_t)c.out % (c.out_dtype == MTPSD_FP8_E4M3 ? 8 : 16)) == 0 && c.out_token_stride % out_vec == 0 &&
-                  (rows || c.out_head_stride % out_vec == 0) && fits16(c.weight) && fits16(c.bias) && fits16(p.cos_sin);
+                  (rows || s->oh % out_vec == 0) && fits16(c.weight) && fits16(c.bias) && fits16(p.cos_sin);
   if (!ok) return -1;
   s->nr = rows ? 4 : p.rot_dim / 16;
   if (rows) s->rot_start = 512;
@@ -495,6 +500,9 @@ int launch_norm_rope(const NormRopePlan& p, cudaStream_t st) {
     if (inst[i] >= 0) {
       if (a.k.in_f32) launch_sides<true>(a, inst[i], inst[i], st);
       else launch_sides<false>(a, inst[i], inst[i], st);
+    } else if (side[i].out_type == MTPSD_FP8_DS_MLA || side[i].out_type == MTPSD_FP4_MLA) {
+      set_error("norm_rope: cache rows need 16-byte aligned rows");   // (refused before: the vector kernel alone writes them)
+      return MTPSD_EUNSUPPORTED;
     } else {
       const int64_t want = ceil_div(p.T * side[i].heads, 8), most = 8 * (int64_t)num_sms();
       const unsigned n = (unsigned)(want < most ? want : most);

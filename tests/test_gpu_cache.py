@@ -359,6 +359,12 @@ def test_norm_rope_into_latent_rows(mt, fmt, dtype, rot):
         kept = [t for t in range(T) if T == 1 or t not in (3, 5)]
         want[dev(slots[kept])] = rows[kept]
         assert torch.equal(cache, want) and st.item() == (0 if T == 1 else STATUS["WRITE_RANGE"])
+        # one head of three dimensions, whose head stride says nothing
+        base = torch.zeros(T * 576 + 8, dtype=dtype, device="cuda")
+        base[:T * 576].view(T, 576).copy_(kv)
+        again = torch.empty(T, fmt, dtype=torch.uint8, device="cuda")
+        mt.norm_rope(pos, cs, k=base.as_strided((T, 1, 576), (576, 577, 1)), k_out=again, **args)
+        assert torch.equal(again, rows)
         # without slots: row t
         straight = torch.empty(T, fmt, dtype=torch.uint8, device="cuda")
         mt.norm_rope(pos, cs, k=kv, k_out=straight, **args)
