@@ -10,22 +10,25 @@
 // positions each CTA sends its partial scores (log2 units, fp16) to the other and adds what it receives to its own fp32 ones.
 // Every selected row is read, and each half of it dequantized, once per cluster.
 //
-// What sets the pace is a pair's chain: QK^T, read the scores, exchange, maximum, exponentials, P to TMEM, PV, and only then
-// the next QK^T into that score buffer; it takes about three times as long as the MMAs.  Two warpgroups therefore take the
-// pairs in turn, each with a score buffer, a receive slot and a staging slot of its own, so that two chains run side by side;
-// the thread that sends a head's scores keeps them in registers for the addition, so TMEM is read once.  The only step in order is
-// the running maximum of a head, which passes between the two threads of that head through shared memory.  The reference maximum is
-// lazy: O is rescaled only when a head's maximum grows by more than 2^8.
+// A pair's chain (QK^T, read the scores, exchange, maximum, exponentials, P to TMEM, PV, and only then the next QK^T into that
+// score buffer) takes several times as long as its MMAs.  Two warpgroups therefore take the pairs in turn, each with a score
+// buffer, a receive slot and a staging slot of its own, so that two chains run side by side; the thread that sends a head's scores keeps
+// them in registers for the addition, so TMEM is read once.  The only step in order is the running maximum of a head, which passes
+// between the two threads of that head through shared memory.  The reference maximum is lazy: O is rescaled only when a head's
+// maximum grows by more than 2^8.
+// Measured (70 rows, one wave): 1.9 us a pair; 1.5 without the dequantization's arithmetic, 1.07 without the gathers too, 0.77
+// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 217 us (FP8 rows: 357).
 //
 //   TMEM  [0,128) this CTA's 256 query dims (A operand, bf16 pairs); [128,192) [192,256) scores of even and odd pairs (fp32), P
 //         over their first 32 columns (bf16 pairs); [256,512) O
 //   SMEM  rope query dims (rank 0, 128-byte swizzle); a ring of three pair buffers of 64 positions in chunks of 64 dims (64 rows x 128
 //         B, 128-byte swizzle): the K-major B operand of the scores and, for chunks 0..3, the MN-major B operand of PV; two
 //         receive slots and two staging slots of 16 KB (two halves of 8 KB: row = head, 32 positions of fp16 in 64 bytes,
-//         16-byte piece c at c ^ ((head >> 1) & 3)); each producer warp's ring of FD gathered tiles
+//         16-byte piece c at c ^ ((head >> 1) & 3)); a ring of FD gathered tiles
 //
-// The producers (four warps) gather the codes and scales of 8 rows per 32-position tile with TMA tile::gather4, FD tiles ahead, and
-// write them as bf16 into the pair buffer; the rope values are bf16 already and are gathered straight into their chunk.
+// Two warps gather the codes and scales with TMA tile::gather4, FD tiles of 32 positions ahead, and the rope values, which are bf16
+// already, straight into their chunk; four warps write the codes as bf16 into the pair buffer.  One warp for both was slower
+// (278 us for the 192 rows): its issue, waits and arithmetic add up to more than the rest of a pair's chain.
 // A row is dequantized as code * scale * 2^-14: the code's bits are shifted to where a bf16 has them (a factor 2^-126), and
 // the scale, times 2^112, is a bf16 too, so one exact multiplication per two values remains.  The factor is taken back in the
 // softmax scale and in the output; the rope queries are multiplied by 2^-14 as well, so that both parts of a score have it.
@@ -46,7 +49,7 @@ namespace m4 {
 
 constexpr int DL = 576, DV = 512, DVH = 256;
 constexpr int HG = 128;                  // heads per CTA (MMA M)
-constexpr int NP = 64;                   // positions per MMA step (a pair of TMA-sized halves: one "pair" below)
+constexpr int NP = 64;                   // positions per MMA step: a pair (of gathered tiles)
 constexpr int NPAIR = 3;                 // pair buffers in the ring
 constexpr int CHUNK = NP * 128;          // 64 dims of a pair buffer
 constexpr int PAIR_STRIDE = 5 * CHUNK;
