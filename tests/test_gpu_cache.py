@@ -580,3 +580,22 @@ def test_caches_of_4_bit_rows_move_and_write_back(mt):
         k = min(int(n_acc[b]) + 1, W)
         moved[slots[b, :k]] = want[slots[b, acc[b, :k]]]
     assert np.array_equal(a.cpu().numpy(), moved)
+
+
+def test_empty_calls(mt):
+    """No tokens, no rows, no selected entries: nothing is written, or zeros and -inf."""
+    z = lambda *sh, dtype=torch.bfloat16: torch.empty(*sh, dtype=dtype, device="cuda")  # noqa: E731
+    cs, pos = dev(rope_table(9, 64)), z(0, dtype=torch.int64)
+    q, k = mt.norm_rope(pos, cs, q=z(0, 4, 128), k=z(0, 128), q_norm="rms")
+    assert q.shape == (0, 4, 128) and k.shape == (0, 128)
+    cache = torch.full((5, 416), 7, dtype=torch.uint8, device="cuda")
+    mt.norm_rope(pos, cs, k=z(0, 576), k_rot_start=512, k_out=cache, slots=pos)
+    mt.pack_latent_fp4(z(0, 576), cache, slots=pos)
+    assert mt.pack_latent_fp4(z(0, 576)).shape == (0, 416) and (cache == 7).all()
+    for H in (16, 128):
+        lse = torch.zeros(2, H, device="cuda")
+        out = mt.sparse_mla_decode(torch.ones(2, H, 576, dtype=torch.bfloat16, device="cuda"), cache, dev([0]), u32([0, 2]), dev([3, 4]),
+                                   z(2, 0, dtype=torch.int32), SCALE, lse=lse)
+        assert (out == 0).all() and (lse == -math.inf).all()
+        none = mt.sparse_mla_decode(z(0, H, 576), cache, dev([0]), u32([0, 0]), pos, z(0, 8, dtype=torch.int32), SCALE)
+        assert none.shape == (0, H, 512)
