@@ -17,7 +17,7 @@
 // between the two threads of that head through shared memory.  The reference maximum is lazy: O is rescaled only when a head's
 // maximum grows by more than 2^8.
 // Measured (70 rows, one wave): 1.9 us a pair; 1.5 without the dequantization's arithmetic, 1.07 without the gathers too, 0.77
-// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 217 us (FP8 rows: 357).
+// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 213 us (FP8 rows: 357).
 //
 //   TMEM  [0,128) this CTA's 256 query dims (A operand, bf16 pairs); [128,192) [192,256) scores of even and odd pairs (fp32), P
 //         over their first 32 columns (bf16 pairs); [256,512) O
@@ -67,7 +67,7 @@ constexpr int OFF_MREF = OFF_MASK + 32;               // [128] reference maxima
 constexpr int OFF_ML = OFF_MREF + HG * 4;             // [2][128] (reference, sum) of the warpgroups
 constexpr int OFF_BAR = OFF_ML + 2 * HG * 8;
 constexpr int B_CFULL = 0, B_CEMPTY = B_CFULL + NPAIR, B_SFULL = B_CEMPTY + NPAIR, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
-              B_XFULL = B_PVDONE + 2, B_XFREE = B_XFULL + 4, B_DEC = B_XFREE + 2, B_FFULL = B_DEC + 8, B_FEMPTY = B_FFULL + FD, B_QREADY = B_FEMPTY + FD, B_DRAIN = B_QREADY + 1,
+              B_XFULL = B_PVDONE + 2, B_XFREE = B_XFULL + 4, B_DEC = B_XFREE + 2, B_FFULL = B_DEC + 8, B_FEMPTY = B_FFULL + FD / 2, B_QREADY = B_FEMPTY + FD / 2, B_DRAIN = B_QREADY + 1,
               N_BARS = B_DRAIN + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;      // and room to align
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bar_init(&x_free[i], 4);             // one arrival per warp of the other CTA's warpgroup
     }
     for (int i = 0; i < 8; ++i) bar_init(&dec[i], 1);
-    for (int i = 0; i < FD; ++i) {
+    for (int i = 0; i < FD / 2; ++i) {     // per pair of tiles
       bar_init(&f_full[i], N_GATHER);
       bar_init(&f_empty[i], N_DEQ);
     }
@@ -618,11 +618,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t src_scale = saddr(sm + OFF_F) + F_SCL + 2 * dw * 128 + sub * 16 + 2 * j;
     for (int P = 0; P < n_pairs; ++P) {
       const int q = P % NPAIR, n = P / NPAIR, f0 = (2 * P) % FD;
-      const uint32_t fpar = ((2 * P) / FD) & 1;
       uint4 cd[4];
       uint32_t scl[4];
-      bool ok = wait_all(&f_full[f0], fpar, abort_flag, p.status) && wait_all(&f_full[f0 + 1], fpar, abort_flag, p.status);
-      if (!ok) break;
+      if (!wait_all(&f_full[P % (FD / 2)], (P / (FD / 2)) & 1, abort_flag, p.status)) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {        // tile i / 2, rows + 4 (i % 2)
         const uint32_t at = (uint32_t)(f0 + (i >> 1)) * F_TILE;
@@ -658,8 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         bar_arrive(&c_full[q]);
-        bar_arrive(&f_empty[f0]);
-        bar_arrive(&f_empty[f0 + 1]);
+        bar_arrive(&f_empty[P % (FD / 2)]);
       }
     }
   } else if (warp < MMA_WARP) {
@@ -684,7 +681,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     int32_t pg1 = PAGED ? page_entry(p, breq, s1) : -1;
     int32_t row = 0;                       // pool rows of the present block (a row outside the map reads zeros)
     uint32_t there = 0;                    // which of them are there
-    int done = 0;                          // tiles whose gathers have been issued
     for (int t = 0; t < n_tiles; ++t) {
       if (t % 2 == 0) {                    // the next block becomes the present one
         const int blk = t / 2;
@@ -705,18 +701,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[i] = __shfl_sync(0xffffffffu, row, 16 * (t & 1) + i);
       const int f = t % FD, P = t >> 1, q = P % NPAIR, n = P / NPAIR;
-      if (t >= FD && !wait_all(&f_empty[f], (t / FD - 1) & 1, abort_flag, p.status)) break;
+      if (t >= FD && !(t & 1) && !wait_all(&f_empty[P % (FD / 2)], (t / FD - 1) & 1, abort_flag, p.status)) break;
       const uint32_t dst = saddr(sm + OFF_F + f * F_TILE);
       if (elect_one()) {
-        bar_arrive_tx(&f_full[f], 16 * (128 + 16));
+        uint64_t* const full = &f_full[P % (FD / 2)];
+        if (t & 1) bar_arrive_tx(full, 16 * (128 + 16));
+        else bar_expect_tx(full, 16 * (128 + 16));
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          gather4(dst + (4 * gw + g) * 512, &tm_codes, (int)rank * 128, y + 4 * g, &f_full[f]);
-          gather4(dst + F_SCL + (4 * gw + g) * 128, &tm_scale, lat4::OFF_SCALE + (int)rank * 16, y + 4 * g, &f_full[f]);
+          gather4(dst + (4 * gw + g) * 512, &tm_codes, (int)rank * 128, y + 4 * g, full);
+          gather4(dst + F_SCL + (4 * gw + g) * 128, &tm_scale, lat4::OFF_SCALE + (int)rank * 16, y + 4 * g, full);
         }
       }
       __syncwarp();
-      done = t + 1;
       // validity bits and (rank 0) the rope values, straight into their chunk, once the pair buffer is free
       if (n > 0 && !(t & 1) && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) break;
       if (lane == 0) *(uint16_t*)(mask_s + 8 * q + 4 * (t & 1) + 2 * gw) = (uint16_t)(there >> (16 * (t & 1)));
@@ -733,10 +730,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       __syncwarp();
-    }
-    if (*abort_flag && lane == 0) {        // copies in flight land before exit (waits bounded once more)
-      volatile int dummy = 0;
-      for (int t = max(0, done - FD); t < done; ++t) mbar::wait<false>(&f_full[t % FD], (t / FD) & 1, &dummy, p.status, WAIT_NS);
     }
   } else {
     // ------------------------------------------------ MMA issue: QK(0), then for every pair P QK(P + 1) and PV(P)
