@@ -418,7 +418,7 @@ def kv_writeback(src_latent, src_idxk, src_idxs, num_accepted, dst_latent, dst_i
         _need(dst_idxs, "dst_idxs", torch.float32)
     check("mtpsd_kv_writeback", lib().mtpsd_kv_writeback(
         _ptr(src_latent), _ptr(src_idxk), _ptr(src_idxs), B, W,
-        _latent_dtype(src_latent), idx_dim,
+        _latent_dtype(src_latent, dst_latent), idx_dim,
         _ptr(num_accepted), _ptr(dst_latent), _ptr(dst_idxk), _ptr(dst_idxs), _ptr(cache_start), _ptr(dst_pos),
         dst_latent.shape[0], _ptr(next_pos), _ptr(dev_status), _stream(stream)))
     return next_pos
@@ -448,10 +448,19 @@ def topk_share_gather(step0_topk, row_offsets, num_accepted=None, shared_idx=Non
 
 # --------------------------------------------------------------------------- paged caches
 
-def _latent_dtype(t):
-    if t.dtype == torch.uint8:
-        return N.MTPSD_FP4_MLA if t.shape[-1] == 416 else N.MTPSD_FP8_DS_MLA
-    return N.MTPSD_BF16 if t.dtype == torch.bfloat16 else N.MTPSD_F32
+_LATENT_TYPES = {(torch.bfloat16, 576): N.MTPSD_BF16, (torch.float32, 576): N.MTPSD_F32, (torch.uint8, 656): N.MTPSD_FP8_DS_MLA,
+                 (torch.uint8, 416): N.MTPSD_FP4_MLA}
+
+
+def _latent_dtype(t, dst=None):
+    """The type of latent rows (the last dim); dst: the cache that such rows are written to."""
+    dt = _LATENT_TYPES.get((t.dtype, t.shape[-1]))
+    if dt is None:
+        raise ValueError("latent rows must be 576 bfloat16 or float32 values, or 656 (FP8) or 416 (4-bit) bytes, got "
+                         f"{t.shape[-1]} of {t.dtype}")
+    if dst is not None and dst.shape[-1] != t.shape[-1]:
+        raise ValueError(f"rows of {t.shape[-1]} cannot be written to a cache whose rows have {dst.shape[-1]}")
+    return dt
 
 
 def assign_cache_locs(block_table, page_size: int, start_pos, W: int, out_cache_loc=None, dev_status=None,
@@ -504,7 +513,7 @@ def kv_writeback_slots(src_latent, src_idxk, src_idxs, num_accepted, dst_latent,
         _need(src_idxs, "src_idxs", torch.float32)
         _need(dst_idxs, "dst_idxs", torch.float32)
     check("mtpsd_kv_writeback_slots", lib().mtpsd_kv_writeback_slots(
-        _ptr(src_latent), _ptr(src_idxk), _ptr(src_idxs), B, W, _latent_dtype(src_latent), idx_dim,
+        _ptr(src_latent), _ptr(src_idxk), _ptr(src_idxs), B, W, _latent_dtype(src_latent, dst_latent), idx_dim,
         _ptr(num_accepted), _ptr(dst_latent), _ptr(dst_idxk), _ptr(dst_idxs), _ptr(dst_slots), dst_latent.shape[0],
         _ptr(dst_pos), _ptr(next_pos), _ptr(dev_status), _stream(stream)))
     return next_pos
