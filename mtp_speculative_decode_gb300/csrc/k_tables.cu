@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) block_table_release_kernel(int32_t* t
     const int64_t o = old_len[b], k = keep_len ? keep_len[b] : 0;
     if (o < 0 || k < 0 || o > ((int64_t)stride << shift)) return false;
     *hi = (int)pages_of(o, shift);
-    *lo = (int)min((int64_t)*hi, pages_of(k, shift));
+    *lo = (int)pages_of(min(k, o), shift);   // (a length near 2^63, "all of them", has no page count)
     return true;
   };
   for (int b = warp; b < B; b += THREADS / 32) {

@@ -1,0 +1,36 @@
+"""Calls that fill and read the caches, at the edges of what they document: lengths without a bound, request counts at the limits of
+shared memory, values next to zero, misaligned buffers, padded batches, layers on several streams.  Each against the float64
+oracle or the exact result."""
+import math
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8 as ofp8
+from oracle import latent4 as o4
+from oracle import paged as opaged
+from oracle import tables as otab
+from test_gpu_cache import SCALE, STATUS, check_mla, dev, i32, mla_case, mt, status, rope_table, table_case, u32  # noqa: F401
+from test_gpu_cache_step import tokens
+
+pytestmark = pytest.mark.gpu
+
+# ----------------------------------------------------------------------------- block tables
+
+@pytest.mark.parametrize("keep_len", [2 ** 63 - 1, 2 ** 63 - 64, 2 ** 62, 2 ** 32 + 5])
+@pytest.mark.parametrize("ps", [1, 64])
+def test_release_keeping_more_than_any_length(mt, ps, keep_len):  # noqa: F811
+    """The largest int64 says that a request keeps everything: its pages stay, the others' go."""
+    rng = np.random.default_rng(ps)
+    t, old, _, free = table_case(rng, 6, ps, 20, 20 * ps, True)
+    free, n_free = np.concatenate([free, np.full(120, -3, np.int32)]), len(free)
+    keep = np.array([keep_len, 0, keep_len, 3, keep_len, 0], np.int64)
+    d_t, d_f, d_n, st = dev(t), dev(free), i32([n_free]), status()
+    mt.block_table_release(d_t, ps, dev(old), d_f, d_n, keep_len=dev(keep), dev_status=st)
+    w_t, w_f, w_n, w_st = otab.release(t, ps, old, free, n_free, keep)
+    assert w_st == 0 and st.item() == 0 and d_n.item() == w_n > n_free
+    assert np.array_equal(d_t.cpu().numpy(), w_t) and np.array_equal(d_f.cpu().numpy(), w_f)
