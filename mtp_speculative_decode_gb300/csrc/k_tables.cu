@@ -325,14 +325,16 @@ int launch_block_table_grow(const mtpsd_block_table_args& c, int shift, cudaStre
     a.n_free_out = nullptr;
     a.lengths = nullptr;
   }
-  const size_t smem = sizeof(Share) * (size_t)a.B;
+  // (asked for whatever B is: the 48 KB that need no asking hold the kernel's static shared memory too)
   static std::atomic<uint64_t> attr{0};
-  if (smem > 48 * 1024 && !set_smem_limit_once(block_table_grow_kernel, (int)(sizeof(Share) * TABLES_MAX_B), attr)) {
+  if (!set_smem_limit_once(block_table_grow_kernel, (int)(sizeof(Share) * TABLES_MAX_B), attr)) {
     set_error("block_table_grow: cudaFuncSetAttribute failed");
     return MTPSD_ECUDA;
   }
-  launch_k(block_table_grow_kernel, grid, THREADS, smem, st, a);
+  launch_k(block_table_grow_kernel, grid, THREADS, sizeof(Share) * (size_t)a.B, st, a);
   if (finish) {
+    // lengths and the free count move only behind tables that were written
+    if (int rc = check_launch("block_table_grow")) return rc;
     a.n_free_out = c.n_free_out;
     a.lengths = c.lengths;
     launch_k(block_table_finish_kernel, 1, THREADS, 0, st, a);

@@ -34,3 +34,17 @@ def test_release_keeping_more_than_any_length(mt, ps, keep_len):  # noqa: F811
     w_t, w_f, w_n, w_st = otab.release(t, ps, old, free, n_free, keep)
     assert w_st == 0 and st.item() == 0 and d_n.item() == w_n > n_free
     assert np.array_equal(d_t.cpu().numpy(), w_t) and np.array_equal(d_f.cpu().numpy(), w_f)
+
+
+@pytest.mark.parametrize("B", [4073, 4074, 4096, 4097])
+def test_grow_with_request_counts_at_the_limit_of_shared_memory(mt, B):  # noqa: F811
+    """Each count in a process of its own: what an earlier call asked for holds for the rest of a process."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import numpy as np, mtp_speculative_decode_gb300 as m\n"
+            "from test_gpu_cache import check_grow, table_case\n"
+            "t, old, new, free = table_case(np.random.default_rng(%d), %d, 4, 3, 12, True)\n"
+            "for in_place in (True, False):\n"
+            "    check_grow(m, t, 4, new, free, len(free), old, in_place, [1] * %d)\n" % (os.path.dirname(here), here, B, B, B))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
