@@ -283,7 +283,8 @@ size_t mtpsd_sparse_mla_workspace_size(int32_t R, int32_t n_heads, int32_t n_idx
  * run of 64-position pairs across rows; a row cut between two clusters leaves float32 pieces in the
  * workspace that a second kernel merges.  The count assumes the tensor-core kernel, which needs q,
  * latent, out and workspace 16-byte aligned (TMA loads and stores); other calls run the portable
- * kernel.  0 for sizes that launch nothing.  The workspace size covers every plan. */
+ * kernel, for which q and latent are 16-byte aligned, a workspace that it needs 8 (4 for MTPSD_F32) and out 4.
+ * 0 for sizes that launch nothing.  The workspace size covers every plan. */
 int32_t mtpsd_sparse_mla_launch_count(int32_t R, int32_t n_heads, int32_t n_idx, int32_t n_append, int32_t dtype);
 int mtpsd_sparse_mla_decode(const mtpsd_mla_args* args, void* stream);
 

@@ -462,7 +462,7 @@ template <typename OutT>
 static int launch_combine(const MlaPlan& p, int n_splits, int halves, const float* part_o, const float* part_ml,
                           cudaStream_t st) {
   const int64_t rh = (int64_t)p.R * p.H;
-  if (p.d_v == MLA_DV && ((uintptr_t)p.out % 16) == 0) {
+  if (p.d_v == MLA_DV && (((uintptr_t)p.out | (uintptr_t)part_o) % 16) == 0) {
     launch_k(mla_combine512_kernel<OutT>, (unsigned)((rh + 3) / 4), 256, 0, st, p, n_splits, halves, part_o, part_ml);
   } else {
     launch_k(mla_combine_kernel<OutT>, (unsigned)rh, 128, 0, st, p, n_splits, halves, part_o, part_ml);
@@ -648,6 +648,10 @@ int launch_sparse_mla(const MlaPlan& p, cudaStream_t st) {
     if (!p.ws || p.ws_bytes < need) {
       set_error("sparse_mla_decode: workspace of %zu bytes needed, %zu given", need, p.ws_bytes);
       return MTPSD_EWORKSPACE;
+    }
+    if ((uintptr_t)p.ws % (p.dtype == MTPSD_F32 ? 4 : 8)) {   // partials are stored two at a time
+      set_error("sparse_mla_decode: workspace must be 8-byte aligned (4 for MTPSD_F32)");
+      return MTPSD_EINVAL;
     }
     part_o = (float*)p.ws;
     part_ml = part_o + (size_t)p.R * p.H * sp.n_splits * MLA_DV;

@@ -10,10 +10,13 @@ import numpy as np
 import pytest
 import torch
 
+from mtp_speculative_decode_gb300 import _native as N
 from oracle import fp8 as ofp8
 from oracle import latent4 as o4
+from oracle import mla as omla
 from oracle import paged as opaged
 from oracle import tables as otab
+import parity
 from test_gpu_cache import SCALE, STATUS, check_mla, dev, i32, mla_case, mt, status, rope_table, table_case, u32  # noqa: F401
 from test_gpu_cache_step import tokens
 
@@ -48,3 +51,38 @@ def test_grow_with_request_counts_at_the_limit_of_shared_memory(mt, B):  # noqa:
             "    check_grow(m, t, 4, new, free, len(free), old, in_place, [1] * %d)\n" % (os.path.dirname(here), here, B, B, B))
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16", "f32"])
+def test_mla_with_a_misaligned_workspace(mt, kind):  # noqa: F811
+    """Split partials at any multiple of 8 bytes: joined by loads that such a buffer allows; at less the call is refused."""
+    rng = np.random.default_rng(15)
+    H = 16 if kind == "f32" else 128
+    q, rows, caps, start, pos, idx = mla_case(rng, 1, 2, H, 2048, [5000])
+    dt = {"fp4": N.MTPSD_FP4_MLA, "fp8": N.MTPSD_FP8_DS_MLA, "bf16": N.MTPSD_BF16, "f32": N.MTPSD_F32}[kind]
+    c = o4.unpack(rows)
+    latent = dev(rows) if kind == "fp4" else torch.tensor(c, dtype=torch.float32).cuda()
+    if kind == "fp8":
+        latent = mt.pack_latent_fp8(latent)
+        c = omla.unpack_fp8_ds_mla(latent.cpu().numpy())
+    elif kind == "bf16":
+        latent = latent.bfloat16()
+    qd = q.float() if kind == "f32" else q
+    want = omla.sparse_mla(q, c, start, [0, 0], idx, SCALE)
+    need = mt.sparse_mla_workspace_size(2, H, 2048, 0, dt)
+    assert need > 0
+    for off in (0, 8, 16, 24, 4, 1):
+        buf = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
+        ws, st = buf[off:off + need], status()
+        call = lambda: mt.sparse_mla_decode(qd.cuda(), latent, dev(start), u32([0, 2]), dev(pos), dev(idx), SCALE,  # noqa: E731
+                                            workspace=ws, dev_status=st)
+        if off % (4 if kind == "f32" else 8):
+            with pytest.raises(RuntimeError, match="aligned"):
+                call()
+            torch.cuda.synchronize()
+            assert (buf == 0xff).all()
+            continue
+        out = call()
+        assert st.item() == 0 and (buf[:off] == 0xff).all() and (buf[off + need:] == 0xff).all()
+        for r, (o, _) in want.items():
+            parity.check_attention_row(out[r].float().cpu().numpy(), o, parity.ATT_TOL_F32 if kind == "f32" else parity.ATT_TOL_BF16)
