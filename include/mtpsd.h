@@ -102,7 +102,7 @@ int mtpsd_resolve_indexer_types(int32_t n_layers, const char* pattern, int32_t f
  * contiguous values.  [P3] "Indexer 的结构与计算流程" (q and k quantized to FP8
  * with block size 128) and "双 KV 缓存" (float32 scale per token).
  *   x [n_blocks*128] float32 -> codes [n_blocks*128] uint8, scales [n_blocks] float32
- * scale = amax/448 (1 when amax == 0), code = round-to-nearest-even,
+ * scale = amax/448 (1 when that is 0 in float32), code = round-to-nearest-even,
  * saturating, of x/scale (float32 division).
  */
 int mtpsd_quantize_fp8_block128(const float* x, int64_t n_blocks, uint8_t* codes, float* scales,

@@ -140,6 +140,13 @@ inline bool set_smem_limit_once(Kernel kernel, int bytes, std::atomic<uint64_t>&
   return true;
 }
 
+// Scale of a block of FP8 codes whose largest magnitude is m: m / 448, but 1 where that is nothing (m is 0, or so near to it that
+// the quotient rounds to 0: dividing by it would make NaN of the block's zeros).
+__device__ __forceinline__ float fp8_block_scale(float m) {
+  const float s = __fdiv_rn(m, 448.0f);
+  return s > 0.f ? s : 1.0f;
+}
+
 // Order-preserving map of a float to uint32 (larger float -> larger key).
 __device__ __forceinline__ uint32_t float_key(float f) {
   uint32_t u = __float_as_uint(f == 0.f ? 0.f : f);   // -0 and +0 compare equal

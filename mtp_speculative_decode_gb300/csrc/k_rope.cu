@@ -123,7 +123,6 @@ __device__ __forceinline__ float amax8(const float* v, float m) {
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
   return m;
 }
-__device__ __forceinline__ float fp8_scale(float m) { return m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f; }
 
 // A token's output row and whether it is there; flagged by the caller's lane 0.
 __device__ __forceinline__ bool token_ok(const Args& a, const Side& s, int64_t t, int64_t* row, int64_t* pos, int32_t* bits) {
@@ -282,7 +281,7 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) m = amax8(v[i], m);
-      const float scale = fp8_scale(group_max(m, L));
+      const float scale = fp8_block_scale(group_max(m, L));
       if (on) {
         uint8_t* o = (uint8_t*)s.out + row * s.ot + h * s.oh;
 #pragma unroll
@@ -299,7 +298,7 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
         if (eight) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float scale = fp8_scale(group_max(amax8(v[2 + j], 0.f), 16));   // a block of 128: 16 lanes
+            const float scale = fp8_block_scale(group_max(amax8(v[2 + j], 0.f), 16));   // a block of 128: 16 lanes
             if (on) {
               *(uint2*)(o + 256 * j + 8 * lane) = codes8(v[2 + j], scale);
               if ((lane & 15) == 0) *(float*)(o + 512 + 4 * (2 * j + (lane >> 4))) = scale;
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(256) norm_rope_elements_kernel(const __grid_co
     if (s.out_type == MTPSD_FP8_E4M3) {
       float m = 0.f;
       for (int i = lane; i < s.D; i += 32) m = fmaxf(m, fabsf(v[i]));
-      const float scale = fp8_scale(group_max(m, 32));
+      const float scale = fp8_block_scale(group_max(m, 32));
       for (int i = lane; i < s.D; i += 32)
         ((uint8_t*)s.out)[base + i] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(v[i], scale), __NV_SATFINITE, __NV_E4M3);
       if (lane == 0) s.scale[row * s.heads + h] = scale;

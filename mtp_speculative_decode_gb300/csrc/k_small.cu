@@ -64,7 +64,7 @@ __global__ void quantize_fp8_kernel(const float4* __restrict__ x, int64_t n_bloc
     float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float scale = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
+    float scale = fp8_block_scale(m);
     uint32_t c0 = __nv_cvt_float_to_fp8(__fdiv_rn(v.x, scale), __NV_SATFINITE, __NV_E4M3);
     uint32_t c1 = __nv_cvt_float_to_fp8(__fdiv_rn(v.y, scale), __NV_SATFINITE, __NV_E4M3);
     uint32_t c2 = __nv_cvt_float_to_fp8(__fdiv_rn(v.z, scale), __NV_SATFINITE, __NV_E4M3);
@@ -111,7 +111,7 @@ __global__ void pack_latent_fp8_kernel(const void* __restrict__ latent, int64_t 
       float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
       for (int sh = 16; sh; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-      const float scale = m > 0.f ? __fdiv_rn(m, 448.0f) : 1.0f;
+      const float scale = fp8_block_scale(m);
       uint32_t c = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -76,7 +76,7 @@ def quantize_block128(x: np.ndarray):
     """Dynamic block-128 FP8 quantization of the last axis.
 
     For every block of 128 contiguous elements: amax = max |x|;
-    scale = amax / 448 (scale = 1 when amax == 0); code = RNE-satfinite(x / scale).
+    scale = amax / 448 (1 when that is 0 in float32); code = RNE-satfinite(x / scale).
     The scale and the division are float32 operations (the scale is stored as
     float32 per [P3] "双 KV 缓存"), so the result is defined bit for bit.
 
@@ -89,7 +89,8 @@ def quantize_block128(x: np.ndarray):
         raise ValueError("last axis must be a multiple of 128")
     xb = x.reshape(x.shape[:-1] + (n // BLOCK, BLOCK))
     amax = np.max(np.abs(xb), axis=-1)
-    scale = np.where(amax > 0, amax / np.float32(E4M3_MAX), np.float32(1.0)).astype(np.float32)
+    scale = amax / np.float32(E4M3_MAX)
+    scale = np.where(scale > 0, scale, np.float32(1.0)).astype(np.float32)
     y = (xb / scale[..., None]).astype(np.float32)
     codes = encode_e4m3_rne_satfinite(y.astype(np.float64))
     return codes.reshape(x.shape), scale

@@ -53,6 +53,44 @@ def test_grow_with_request_counts_at_the_limit_of_shared_memory(mt, B):  # noqa:
     assert res.returncode == 0, res.stderr[-2000:]
 
 
+# ----------------------------------------------------------------------------- norms, rotation, codes
+
+@pytest.mark.parametrize("kind", ["quantizer", "heads", "elements", "rows", "pack"])
+def test_scales_of_values_next_to_zero(mt, kind):  # noqa: F811
+    """The largest magnitude of a block over 448 in float32 has no value left below about 3e-43: the scale is then 1, as for a block
+    of zeros, and the codes are zeros that keep their signs."""
+    step = 2.0 ** -149
+    top = np.array([0, 1, 200, 223, 225, 448, 630, 700, 10000]) * step
+    x = np.zeros((len(top), 128))
+    x[:, 3], x[:, 70], x[:, 127] = top, -top / 2, -step * (top > 0)
+    x = x.astype(np.float32)
+    amax = np.abs(x).max(1)
+    scale = amax / np.float32(448)
+    scale = np.where(scale > 0, scale, np.float32(1))
+    codes = ofp8.encode_e4m3_rne_satfinite((x / scale[:, None]).astype(np.float64))
+    assert (scale[:4] == 1).all() and (scale[4:] < 1e-40).all() and (codes[:4] & 127 == 0).all() and (codes[4:] & 127).max() == 126
+    T = len(top)
+    if kind == "quantizer":
+        got, sc = mt.quantize_fp8_block128(dev(x))
+    elif kind in ("heads", "elements"):
+        wide = torch.zeros(T, 129, device="cuda")
+        wide[:, :128] = dev(x)
+        q = dev(x) if kind == "heads" else wide[:, :128]             # (rows off 16 bytes: the kernel for any shape)
+        got, sc = torch.full((T, 128), 9, dtype=torch.uint8, device="cuda"), torch.full((T, 1), 9.0, device="cuda")
+        mt.norm_rope(None, None, q=q, q_out=got, q_scale=sc)
+    else:
+        latent = torch.zeros(T, 576, device="cuda")
+        latent[:, 256:384] = dev(x)
+        packed = torch.full((T, 656), 9, dtype=torch.uint8, device="cuda")
+        if kind == "rows":
+            mt.norm_rope(None, None, k=latent, k_out=packed)
+        else:
+            mt.pack_latent_fp8(latent, packed)
+        got, sc = packed[:, 256:384], packed[:, 520:524].contiguous().view(torch.float32)
+        assert (packed[:, :256] == 0).all() and (packed[:, 384:512] == 0).all()
+    assert np.array_equal(got.cpu().numpy(), codes) and np.array_equal(sc.cpu().numpy().reshape(-1), scale)
+
+
 @pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16", "f32"])
 def test_mla_with_a_misaligned_workspace(mt, kind):  # noqa: F811
     """Split partials at any multiple of 8 bytes: joined by loads that such a buffer allows; at less the call is refused."""
