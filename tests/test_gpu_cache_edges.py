@@ -91,6 +91,30 @@ def test_scales_of_values_next_to_zero(mt, kind):  # noqa: F811
     assert np.array_equal(got.cpu().numpy(), codes) and np.array_equal(sc.cpu().numpy().reshape(-1), scale)
 
 
+@pytest.mark.parametrize("D,rot", [(128, 0), (128, 128), (90, 0), (90, 90)])
+def test_norm_whose_reciprocal_root_is_infinite(mt, D, rot):  # noqa: F811
+    """eps 0 and a head whose squares have no float32 value: x times infinity times the weight, as the formula's three factors give
+    it; zeros give NaN."""
+    x = torch.tensor([1e-30, -3e-25, 0.0, 2e-38, 1e-45]).cuda().repeat(D)[:D].view(1, 1, D).repeat(3, 2, 1)
+    x[1] = torch.randn(2, D, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    w = torch.linspace(0.5, 2, D, device="cuda")
+    w[1], w[8], w[20] = -1.0, 3e38, 0.0
+    pos, cs = (None, None) if not rot else (dev(np.zeros(3, np.int64)), torch.tensor([0.8, 0.6]).cuda().repeat_interleave(rot // 2)[None])
+    got, _ = mt.norm_rope(pos, cs, q=x, q_norm="rms", q_weight=w, eps=0.0)
+    r = torch.rsqrt(x.square().mean(-1, keepdim=True))
+    want = x * r * w
+    size = want.abs()
+    assert r[0].isinf().all() and want[0].isinf().any() and want[0].isnan().any() and r[1].isfinite().all()
+    if rot:
+        a, b = want[..., :rot // 2], want[..., rot // 2:]
+        want = torch.cat([a * 0.8 - b * 0.6, a * 0.6 + b * 0.8], -1)
+        size = (a.abs() + b.abs()).repeat(1, 1, 2)
+    plain = ~want.isfinite()
+    assert plain[0].all() and torch.equal(got.isnan(), want.isnan()) and torch.equal(got[plain].nan_to_num(), want[plain].nan_to_num())
+    # (two sums of up to 128 squares: 2^-17 of each other)
+    assert ((got - want).abs() <= 2.0 ** -15 * size)[~plain].all()
+
+
 @pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16", "f32"])
 def test_mla_with_a_misaligned_workspace(mt, kind):  # noqa: F811
     """Split partials at any multiple of 8 bytes: joined by loads that such a buffer allows; at less the call is refused."""
