@@ -636,7 +636,9 @@ class PagedAttention:
 
     B requests of at most max_len tokens share n_pages pages; H query heads and H_I indexer heads; at most max_tokens tokens a
     step.  The weights are those of the indexer's key norm (128, with its bias) and of the latent's norm (512); cos_sin [n_pos, 64] turns the
-    first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'."""
+    first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'.  The scratch of the largest step is held
+    from the start, about 4 max_tokens max_len bytes for the selection's scores: layers run side by side, and captured steps stay
+    valid beside others."""
 
     def __init__(self, B: int, max_len: int, n_pages: int, page_size: int, cos_sin, k_weight, k_bias, latent_weight, H: int = 128,
                  H_I: int = 64, topk: int = 2048, max_tokens: int = 4096, row_bytes: int = 416, interleaved: bool = True,
@@ -661,6 +663,12 @@ class PagedAttention:
         self.topk_idx = new(T, topk, dtype=torch.int32)
         self.out = new(T, H, 512, dtype=torch.bfloat16)
         self.status = new(1, dtype=torch.int32)
+        # Scratch of its own, for a step of any size: one that is shared, or grown, would be another call's on another stream, and no
+        # longer there when a captured step is replayed.  (The attention of few tokens can need more than that of many: it is split.)
+        mla_dtype = api._latent_dtype(self.latent)
+        mla_bytes = max((api.sparse_mla_workspace_size(t, H, topk, 0, mla_dtype) for t in range(1, T + 1)), default=0)
+        self.idx_ws = new(api.indexer_topk_workspace_size(B, T, max_len, topk), dtype=torch.uint8)
+        self.mla_ws = new(mla_bytes, dtype=torch.uint8)
 
     def step(self, new_len, token_offsets, q_idx, k_idx, w_idx, q, kv, stream=None):
         """new_len [B] int64 (lengths after the step), token_offsets [B+1] uint32; of the step's T tokens: q_idx [T, H_I, 128], k_idx
@@ -680,9 +688,10 @@ class PagedAttention:
                       dev_status=self.status, stream=stream)
         paged = (self.block_table, self.page_size)
         api.indexer_topk(self.q_idx[:T], self.q_scale[:T], w_idx, self.k_cache, self.k_scale, None, token_offsets, pos, self.topk,
-                         self.max_len, topk_idx=self.topk_idx[:T], dev_status=self.status, stream=stream, paged=paged)
+                         self.max_len, topk_idx=self.topk_idx[:T], workspace=self.idx_ws, dev_status=self.status, stream=stream,
+                         paged=paged)
         return api.sparse_mla_decode(q, self.latent, None, token_offsets, pos, self.topk_idx[:T], W.SOFTMAX_SCALE, out=self.out[:T],
-                                     dev_status=self.status, stream=stream, paged=paged)
+                                     workspace=self.mla_ws, dev_status=self.status, stream=stream, paged=paged)
 
     def release(self, keep_len=None):
         """Returns the pages behind keep_len [B] tokens (all of them without it) of every request, on the current stream."""

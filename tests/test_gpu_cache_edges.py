@@ -148,3 +148,85 @@ def test_mla_with_a_misaligned_workspace(mt, kind):  # noqa: F811
         assert st.item() == 0 and (buf[:off] == 0xff).all() and (buf[off + need:] == 0xff).all()
         for r, (o, _) in want.items():
             parity.check_attention_row(out[r].float().cpu().numpy(), o, parity.ATT_TOL_F32 if kind == "f32" else parity.ATT_TOL_BF16)
+
+
+# ----------------------------------------------------------------------------- the layer
+
+def layer(row_bytes, max_len=320, page=16, max_tokens=64, H=32, n_pages=60):
+    from mtp_speculative_decode_gb300 import pipeline
+    rng = np.random.default_rng(5)
+    w = lambda n: dev((1 + 0.2 * rng.normal(size=n)).astype(np.float32))  # noqa: E731
+    return pipeline.PagedAttention(3, max_len, n_pages, page, dev(rope_table(max_len + page, 64)), w(128), w(128), w(512), H=H, H_I=32,
+                                   topk=64, max_tokens=max_tokens, row_bytes=row_bytes)
+
+
+def lens(x):
+    return dev(np.array(x, np.int64))
+
+
+def state(L):
+    return [x.clone() for x in (L.block_table, L.free_pages, L.n_free, L.lengths, L.latent, L.k_cache, L.k_scale)]
+
+
+@pytest.mark.parametrize("row_bytes", [416, 656, 1152])
+def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
+    """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
+    from mtp_speculative_decode_gb300 import api
+    L = layer(row_bytes, H=128)
+    api._default_ws.clear()
+    L.step(lens([5, 0, 9]), u32([0, 5, 5, 14]), **tokens(np.random.default_rng(11), 14, 128))
+    torch.cuda.synchronize()
+    assert not api._default_ws
+
+
+@pytest.mark.parametrize("row_bytes", [416, 656, 1152])
+def test_two_layers_at_once(mt, row_bytes):  # noqa: F811
+    """Layers stepped on two streams at the same time, of different sizes: the bits of a step alone."""
+    rng = np.random.default_rng(12)
+    xs = [tokens(rng, 64, 128), tokens(rng, 9, 128)]
+    new, off = [lens([50, 4, 10]), lens([3, 3, 3])], [u32([0, 50, 54, 64]), u32([0, 3, 6, 9])]
+
+    def step(L, i, s=None):
+        x = {k: v.clone() for k, v in xs[i].items()}
+        torch.cuda.synchronize()
+        return L, L.step(new[i], off[i], **x, stream=s), x
+
+    want = [step(layer(row_bytes, H=128), i)[1].clone() for i in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        layers = [layer(row_bytes, H=128) for _ in range(2)]
+        copies = [{k: v.clone() for k, v in x.items()} for x in xs]
+        torch.cuda.synchronize()
+        got = [layers[i].step(new[i], off[i], **copies[i], stream=(streams[0], streams[1].cuda_stream)[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(L.status.item() == 0 for L in layers)
+
+
+@pytest.mark.parametrize("row_bytes", [416, 656, 1152])
+def test_captured_step_beside_larger_eager_ones(mt, row_bytes):  # noqa: F811
+    """A decode step in a graph, replayed after prompts of other layers and calls of other sizes: its scratch is still its own."""
+    rng = np.random.default_rng(13)
+    x = tokens(rng, 6, 128)
+    q0 = x["q"].clone()
+    new, off = lens([2, 2, 2]), u32([0, 2, 4, 6])
+    M = layer(row_bytes, H=128)
+    for n in (2, 4):
+        want = M.step(lens([n] * 3), off, **{k: v.clone() for k, v in x.items()}).clone()
+    L = layer(row_bytes, H=128)
+    L.step(new, off, **{k: v.clone() for k, v in x.items()})
+    new.fill_(4)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = L.step(new, off, **x)
+    big = layer(row_bytes, H=128, max_len=4000, max_tokens=600, n_pages=400)
+    big.step(lens([500, 60, 40]), u32([0, 500, 560, 600]), **tokens(rng, 600, 128))
+    junk = [torch.full((1 << 22,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):                  # (the tables keep what they have: the step is the same each time)
+        x["q"].copy_(q0)
+        L.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and L.status.item() == 0
+    assert all((j == 0xff).all() for j in junk)
