@@ -38,6 +38,15 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: Optional[int] = None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
+def _torch_stream(stream, device):
+    """A torch stream, or a raw handle as one (None, the current stream, stays None)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream).value or 0
+    # 0 and 1 are the handles of the default stream
+    return torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+
+
 def _empty(stream, *shape, dtype, device) -> torch.Tensor:
     """A new output.  torch's allocator hands a freed block out again in the order of the stream it was allocated on, so
     with a stream given the block has to be that stream's: one of the current stream may still be in use there, and after
@@ -45,10 +54,7 @@ def _empty(stream, *shape, dtype, device) -> torch.Tensor:
     caller is, is recorded as a user of the block, so that it is not handed out while work queued there still reads it."""
     if stream is None:
         return torch.empty(*shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream).value or 0
-        # 0 and 1 are the handles of the default stream
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    stream = _torch_stream(stream, device)
     with torch.cuda.stream(stream):
         t = torch.empty(*shape, dtype=dtype, device=device)
     current = torch.cuda.current_stream(device)

@@ -658,7 +658,8 @@ class PagedAttention:
             raise ValueError("latent rows have 1152 (bf16), 656 (FP8) or 416 (4-bit) bytes")
         self.latent = new(pool, 576, dtype=torch.bfloat16) if row_bytes == 1152 else new(pool, row_bytes, dtype=torch.uint8)
         T = max_tokens
-        self.slots, self.positions = new(T, dtype=torch.int64), new(T, dtype=torch.int64)
+        self.places = new(2, T, dtype=torch.int64)
+        self.slots, self.positions = self.places
         self.q_idx, self.q_scale = new(T, H_I, 128, dtype=torch.uint8), new(T, H_I, dtype=torch.float32)
         self.topk_idx = new(T, topk, dtype=torch.int32)
         self.out = new(T, H, 512, dtype=torch.bfloat16)
@@ -673,9 +674,12 @@ class PagedAttention:
     def step(self, new_len, token_offsets, q_idx, k_idx, w_idx, q, kv, stream=None):
         """new_len [B] int64 (lengths after the step), token_offsets [B+1] uint32; of the step's T tokens: q_idx [T, H_I, 128], k_idx
         [T, 128], w_idx [T, H_I] float32, q [T, H, 576] bf16 (its last 64 dims are turned in place), kv [T, 576].  Returns the
-        attention's output [T, H, 512]."""
+        attention's output [T, H, 512].  Tokens from token_offsets[B] on (a padded batch) have no place: nothing of them is
+        written, their output is 0, and the status gets STATUS_ROW_RANGE."""
         T = q.shape[0]
         slots, pos = self.slots[:T], self.positions[:T]
+        with torch.cuda.stream(api._torch_stream(stream, q.device)):
+            self.places[:, :T].fill_(-1)          # (the table call writes the requests' tokens alone: the rest would keep an earlier step's)
         api.block_table_grow(self.block_table, self.page_size, new_len, self.free_pages, self.n_free, old_len=self.lengths,
                              lengths=self.lengths, token_offsets=token_offsets, slots=slots, positions=pos, dev_status=self.status,
                              stream=stream)

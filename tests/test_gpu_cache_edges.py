@@ -169,6 +169,27 @@ def state(L):
 
 
 @pytest.mark.parametrize("row_bytes", [416, 656, 1152])
+def test_layer_with_a_padded_batch(mt, row_bytes):  # noqa: F811
+    """Tokens behind the last request's: nothing of them reaches the caches (their slots are not those of an earlier step), their
+    outputs are zeros; the others are those of a step without them."""
+    L, M = layer(row_bytes), layer(row_bytes)
+    rng = np.random.default_rng(6)
+    x = tokens(rng, 30, 32)
+    for a in (L, M):
+        a.step(lens([10, 10, 10]), u32([0, 10, 20, 30]), **{k: v.clone() for k, v in x.items()})
+    assert L.status.item() == 0
+    x = tokens(rng, 30, 32)
+    want = M.step(lens([14, 14, 14]), u32([0, 4, 8, 12]), **{k: v[:12].clone() for k, v in x.items()}).clone()
+    out = L.step(lens([14, 14, 14]), u32([0, 4, 8, 12]), **x)
+    assert L.status.item() == STATUS["ROW_RANGE"] and M.status.item() == 0
+    assert all(torch.equal(a, b) for a, b in zip(state(L), state(M)))
+    assert torch.equal(out[:12], want) and (out[12:] == 0).all()
+    fresh = layer(row_bytes)                                     # and in the first step of all
+    fresh.step(lens([2, 0, 0]), u32([0, 2, 2, 2]), **tokens(rng, 9, 32))
+    assert (fresh.k_scale != 0).sum() == 2 and fresh.status.item() == STATUS["ROW_RANGE"]
+
+
+@pytest.mark.parametrize("row_bytes", [416, 656, 1152])
 def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
     """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
     from mtp_speculative_decode_gb300 import api
