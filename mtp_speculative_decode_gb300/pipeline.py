@@ -643,8 +643,19 @@ class PagedAttention:
     def __init__(self, B: int, max_len: int, n_pages: int, page_size: int, cos_sin, k_weight, k_bias, latent_weight, H: int = 128,
                  H_I: int = 64, topk: int = 2048, max_tokens: int = 4096, row_bytes: int = 416, interleaved: bool = True,
                  eps: float = 1e-6):
+        if B < 1 or max_len < 1 or n_pages < 1 or max_tokens < 1 or H < 1 or H % 16 or H_I < 1 or not 1 <= topk <= 4096:
+            raise ValueError("need B, max_len, n_pages, max_tokens and H_I of at least 1, H a multiple of 16, 1 <= topk <= 4096")
+        if not 1 <= page_size <= 65536 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two in 1..65536")
+        if row_bytes not in (1152, 656, 416):
+            raise ValueError("latent rows have 1152 (bf16), 656 (FP8) or 416 (4-bit) bytes")
+        dev, self.row_align = api._current(cos_sin, "cos_sin"), 1 if row_bytes == 1152 else 16      # (what packed rows are made of)
+        for t, name, shape, align in ((cos_sin, "cos_sin", (cos_sin.shape[0], 64), self.row_align), (k_weight, "k_weight", (128,), 1),
+                                      (k_bias, "k_bias", (128,), 1), (latent_weight, "latent_weight", (512,), self.row_align)):
+            self._check(t, name, dev, (torch.float32,), shape, align)
         device = cos_sin.device
-        self.B, self.page_size, self.topk, self.max_len = B, page_size, topk, max_len
+        self.B, self.H, self.H_I, self.max_tokens = B, H, H_I, max_tokens
+        self.page_size, self.topk, self.max_len = page_size, topk, max_len
         self.cos_sin, self.k_weight, self.k_bias, self.latent_weight = cos_sin, k_weight, k_bias, latent_weight
         self.interleaved, self.eps = interleaved, eps
         new = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype, device=device)  # noqa: E731
@@ -654,8 +665,6 @@ class PagedAttention:
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
         self.lengths = new(B, dtype=torch.int64)                # tokens that each request has pages for
         self.k_cache, self.k_scale = new(pool, 128, dtype=torch.uint8), new(pool, dtype=torch.float32)
-        if row_bytes not in (1152, 656, 416):
-            raise ValueError("latent rows have 1152 (bf16), 656 (FP8) or 416 (4-bit) bytes")
         self.latent = new(pool, 576, dtype=torch.bfloat16) if row_bytes == 1152 else new(pool, row_bytes, dtype=torch.uint8)
         T = max_tokens
         self.places = new(2, T, dtype=torch.int64)
@@ -676,7 +685,7 @@ class PagedAttention:
         [T, 128], w_idx [T, H_I] float32, q [T, H, 576] bf16 (its last 64 dims are turned in place), kv [T, 576].  Returns the
         attention's output [T, H, 512].  Tokens from token_offsets[B] on (a padded batch) have no place: nothing of them is
         written, their output is 0, and the status gets STATUS_ROW_RANGE."""
-        T = q.shape[0]
+        T = self._check_step(new_len, token_offsets, q_idx, k_idx, w_idx, q, kv)
         slots, pos = self.slots[:T], self.positions[:T]
         with torch.cuda.stream(api._torch_stream(stream, q.device)):
             self.places[:, :T].fill_(-1)          # (the table call writes the requests' tokens alone: the rest would keep an earlier step's)
@@ -696,6 +705,40 @@ class PagedAttention:
                          paged=paged)
         return api.sparse_mla_decode(q, self.latent, None, token_offsets, pos, self.topk_idx[:T], W.SOFTMAX_SCALE, out=self.out[:T],
                                      workspace=self.mla_ws, dev_status=self.status, stream=stream, paged=paged)
+
+    @staticmethod
+    def _check(t, name, dev, dtypes, shape, align=1, rows=False):
+        """A tensor of the current device: its type and shape, contiguous (rows: its last dim, the rows aligned too)."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device cuda:{dev}, is on {t.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.numel() and not (t.stride(-1) == 1 if rows else t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous")
+        if t.data_ptr() % align or (rows and t.stride(0) * t.element_size() % align):
+            raise ValueError(f"{name} must be {align}-byte aligned")
+
+    def _check_step(self, new_len, token_offsets, q_idx, k_idx, w_idx, q, kv) -> int:
+        """What the calls of a step would refuse, before the first of them has taken pages.  Returns the step's tokens."""
+        dev = api._current(q, "q")
+        T = q.shape[0] if q.dim() else 0
+        if T > self.max_tokens:
+            raise ValueError(f"a step of {T} tokens, at most {self.max_tokens} fit")
+        either = (torch.bfloat16, torch.float32)
+        self._check(q, "q", dev, (torch.bfloat16,), (T, self.H, 576), 16)
+        self._check(new_len, "new_len", dev, (torch.int64,), (self.B,))
+        if new_len.data_ptr() == self.lengths.data_ptr():
+            raise ValueError("new_len must not be the layer's lengths")
+        self._check(token_offsets, "token_offsets", dev, (torch.uint32,), (self.B + 1,))
+        self._check(w_idx, "w_idx", dev, (torch.float32,), (T, self.H_I))
+        self._check(q_idx, "q_idx", dev, either, (T, self.H_I, 128), rows=True)
+        self._check(k_idx, "k_idx", dev, either, (T, 128), rows=True)
+        self._check(kv, "kv", dev, either, (T, 576), self.row_align, rows=True)
+        return T
 
     def release(self, keep_len=None):
         """Returns the pages behind keep_len [B] tokens (all of them without it) of every request, on the current stream."""

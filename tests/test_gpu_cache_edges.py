@@ -189,6 +189,60 @@ def test_layer_with_a_padded_batch(mt, row_bytes):  # noqa: F811
     assert (fresh.k_scale != 0).sum() == 2 and fresh.status.item() == STATUS["ROW_RANGE"]
 
 
+def misfits(x):
+    """name -> arguments of a step that the layer has to refuse."""
+    def but(**kw):
+        return {**x, **kw}
+
+    def off(t):
+        wide = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        return wide[1:].view(t.shape).copy_(t)
+
+    return {"many": {k: torch.cat([v] * 3) for k, v in x.items()}, "kv": but(kv=x["kv"][:-1]), "k_idx": but(k_idx=x["k_idx"][1:]),
+            "q_idx": but(q_idx=x["q_idx"][:, :-1]), "w_idx": but(w_idx=x["w_idx"][:-1]), "w_type": but(w_idx=x["w_idx"].double()),
+            "heads": but(q=x["q"][:, 1:]), "strided": but(q=x["q"].transpose(0, 1).contiguous().transpose(0, 1)),
+            "f32": but(q=x["q"].float()), "kv_width": but(kv=x["kv"][:, :512]), "k_type": but(k_idx=x["k_idx"].half()),
+            "kv_off": but(kv=off(x["kv"])), "q_off": but(q=off(x["q"])), "host": but(w_idx=x["w_idx"].cpu()),
+            "w_strided": but(w_idx=x["w_idx"].t().contiguous().t()), "k_heads": but(k_idx=x["k_idx"].t().contiguous().t())}
+
+
+MISFITS = ["many", "kv", "k_idx", "q_idx", "w_idx", "w_type", "heads", "strided", "f32", "kv_width", "k_type", "kv_off", "q_off", "host",
+           "w_strided", "k_heads"]
+
+
+@pytest.mark.parametrize("name", MISFITS)
+def test_refused_step_leaves_the_layer_as_it_was(mt, name):  # noqa: F811
+    L = layer(416)
+    rng = np.random.default_rng(7)
+    L.step(lens([3, 0, 7]), u32([0, 3, 3, 10]), **tokens(rng, 10, 32))
+    x = tokens(rng, 24, 32)
+    before = state(L)
+    with pytest.raises((ValueError, TypeError)):
+        L.step(lens([11, 8, 15]), u32([0, 8, 16, 24]), **misfits(x)[name])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(state(L), before)) and L.status.item() == 0
+    L.step(lens([11, 8, 15]), u32([0, 8, 16, 24]), **x)
+    assert L.status.item() == 0 and L.lengths.tolist() == [11, 8, 15]
+
+
+def test_refused_lengths_and_layers(mt):  # noqa: F811
+    from mtp_speculative_decode_gb300 import pipeline
+    L = layer(416)
+    x = tokens(np.random.default_rng(8), 6, 32)
+    before = state(L)
+    for new, off in ((lens([6, 0]), u32([0, 6, 6, 6])), (lens([6, 0, 0]), u32([0, 6, 6])), (lens([6, 0, 0]).int(), u32([0, 6, 6, 6])),
+                     (L.lengths, u32([0, 6, 6, 6])), (lens([6, 0, 0]).cpu(), u32([0, 6, 6, 6]))):
+        with pytest.raises((ValueError, TypeError)):
+            L.step(new, off, **x)
+        assert all(torch.equal(a, b) for a, b in zip(state(L), before))
+    cs, w = dev(rope_table(400, 64)), torch.ones(512, device="cuda")
+    args = dict(B=3, max_len=320, n_pages=60, page_size=16, cos_sin=cs, k_weight=w[:128], k_bias=w[:128], latent_weight=w)
+    for bad in (dict(page_size=24), dict(cos_sin=cs[:, :32]), dict(k_weight=w), dict(latent_weight=w.double()), dict(row_bytes=500),
+                dict(B=0), dict(max_len=0), dict(k_bias=w[:127]), dict(max_tokens=0), dict(topk=0), dict(H=20)):
+        with pytest.raises((ValueError, TypeError)):
+            pipeline.PagedAttention(**{**args, **bad})
+
+
 @pytest.mark.parametrize("row_bytes", [416, 656, 1152])
 def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
     """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
