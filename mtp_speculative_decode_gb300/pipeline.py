@@ -634,8 +634,8 @@ class PagedAttention:
     tokens, their slots, norms and rotation straight into the caches (FP8 indexer keys with their scales; latent rows in bf16, 8 or
     4 bits), the indexer's selection and the sparse attention.  Any ragged step: prompt chunks, verify windows, single tokens.
 
-    B requests of at most max_len tokens share n_pages pages; H query heads and H_I indexer heads; at most max_tokens tokens a
-    step.  The weights are those of the indexer's key norm (128, with its bias) and of the latent's norm (512); cos_sin [n_pos, 64] turns the
+    B requests of at most max_len tokens (rounded up to whole pages) share n_pages pages; H query heads and H_I indexer heads; at most
+    max_tokens tokens a step.  The weights are those of the indexer's key norm (128, with its bias) and of the latent's norm (512); cos_sin [n_pos, 64] turns the
     first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'.  The scratch of the largest step is held
     from the start, about 4 max_tokens max_len bytes for the selection's scores: layers run side by side, and captured steps stay
     valid beside others."""
@@ -655,12 +655,13 @@ class PagedAttention:
             self._check(t, name, dev, (torch.float32,), shape, align)
         device = cos_sin.device
         self.B, self.H, self.H_I, self.max_tokens = B, H, H_I, max_tokens
-        self.page_size, self.topk, self.max_len = page_size, topk, max_len
+        self.page_size, self.topk = page_size, topk
+        self.max_len = -(-max_len // page_size) * page_size     # the tables take lengths up to the last page's end
         self.cos_sin, self.k_weight, self.k_bias, self.latent_weight = cos_sin, k_weight, k_bias, latent_weight
         self.interleaved, self.eps = interleaved, eps
         new = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype, device=device)  # noqa: E731
         pool = n_pages * page_size
-        self.block_table = torch.full((B, -(-max_len // page_size)), -1, dtype=torch.int32, device=device)
+        self.block_table = torch.full((B, self.max_len // page_size), -1, dtype=torch.int32, device=device)
         self.free_pages = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
         self.lengths = new(B, dtype=torch.int64)                # tokens that each request has pages for
@@ -677,7 +678,7 @@ class PagedAttention:
         # longer there when a captured step is replayed.  (The attention of few tokens can need more than that of many: it is split.)
         mla_dtype = api._latent_dtype(self.latent)
         mla_bytes = max((api.sparse_mla_workspace_size(t, H, topk, 0, mla_dtype) for t in range(1, T + 1)), default=0)
-        self.idx_ws = new(api.indexer_topk_workspace_size(B, T, max_len, topk), dtype=torch.uint8)
+        self.idx_ws = new(api.indexer_topk_workspace_size(B, T, self.max_len, topk), dtype=torch.uint8)
         self.mla_ws = new(mla_bytes, dtype=torch.uint8)
 
     def step(self, new_len, token_offsets, q_idx, k_idx, w_idx, q, kv, stream=None):

@@ -243,6 +243,18 @@ def test_refused_lengths_and_layers(mt):  # noqa: F811
             pipeline.PagedAttention(**{**args, **bad})
 
 
+def test_layer_lengths_up_to_the_last_page(mt):  # noqa: F811
+    """max_len ends inside a page: a length that the tables accept is seen whole by the selection."""
+    rng = np.random.default_rng(9)
+    x = tokens(rng, 128, 32)
+    got = []
+    for max_len in (100, 128):
+        L = layer(416, max_len=max_len, page=64, max_tokens=128)
+        got.append(L.step(lens([128, 0, 0]), u32([0, 128, 128, 128]), **{k: v.clone() for k, v in x.items()}).clone())
+        assert L.status.item() == 0 and (L.topk_idx[127] >= 100).any() and (L.topk_idx[:128].max(1).values <= dev(np.arange(128))).all()
+    assert torch.equal(*got)
+
+
 @pytest.mark.parametrize("row_bytes", [416, 656, 1152])
 def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
     """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
