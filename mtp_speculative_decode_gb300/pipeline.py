@@ -693,6 +693,8 @@ class PagedAttention:
         api.block_table_grow(self.block_table, self.page_size, new_len, self.free_pages, self.n_free, old_len=self.lengths,
                              lengths=self.lengths, token_offsets=token_offsets, slots=slots, positions=pos, dev_status=self.status,
                              stream=stream)
+        if T == 0:
+            return self.out[:0]
         api.norm_rope(pos, self.cos_sin, q=q_idx, q_out=self.q_idx[:T], q_scale=self.q_scale[:T], k=k_idx, k_norm="layer",
                       k_weight=self.k_weight, k_bias=self.k_bias, k_out=self.k_cache, k_scale=self.k_scale, slots=slots, eps=self.eps,
                       dev_status=self.status, stream=stream)

@@ -243,6 +243,14 @@ def test_refused_lengths_and_layers(mt):  # noqa: F811
             pipeline.PagedAttention(**{**args, **bad})
 
 
+def test_layer_step_without_tokens(mt):  # noqa: F811
+    L = layer(416)
+    x = tokens(np.random.default_rng(16), 4, 32)
+    L.step(lens([4, 0, 0]), u32([0, 4, 4, 4]), **x)
+    out = L.step(lens([4, 20, 0]), u32([0, 0, 0, 0]), **{k: v[:0] for k, v in x.items()})
+    assert out.shape == (0, 32, 512) and L.status.item() == 0 and L.lengths.tolist() == [4, 20, 0] and L.n_free.item() == 57
+
+
 def test_layer_lengths_up_to_the_last_page(mt):  # noqa: F811
     """max_len ends inside a page: a length that the tables accept is seen whole by the selection."""
     rng = np.random.default_rng(9)
