@@ -750,4 +750,5 @@ class PagedAttention:
         if keep_len is None:
             self.lengths.zero_()
         else:
-            torch.minimum(self.lengths, keep_len, out=self.lengths)
+            # (the call leaves a request with a negative length as it was)
+            torch.minimum(self.lengths, torch.where(keep_len < 0, self.lengths, keep_len), out=self.lengths)

@@ -263,6 +263,19 @@ def test_layer_lengths_up_to_the_last_page(mt):  # noqa: F811
     assert torch.equal(*got)
 
 
+def test_layer_release_of_lengths_that_are_none(mt):  # noqa: F811
+    """A negative length releases nothing (flagged) and is not taken over; the largest one keeps everything."""
+    L = layer(416)
+    L.step(lens([20, 5, 40]), u32([0, 20, 25, 60]), **{k: v[:60] for k, v in tokens(np.random.default_rng(10), 60, 32).items()})
+    table, n_free = L.block_table.clone(), L.n_free.item()
+    keep = lens([-1, 2 ** 63 - 1, 17])
+    L.release(keep)
+    assert L.lengths.tolist() == [20, 5, 17] and L.n_free.item() == n_free + 1 and L.status.item() == STATUS["ROW_RANGE"]
+    assert torch.equal(L.block_table[:2], table[:2]) and (L.block_table[2, 2:] == -1).all()
+    L.release()
+    assert L.n_free.item() == 60 and (L.block_table == -1).all() and (L.lengths == 0).all()
+
+
 @pytest.mark.parametrize("row_bytes", [416, 656, 1152])
 def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
     """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
