@@ -743,12 +743,13 @@ class PagedAttention:
         self._check(kv, "kv", dev, either, (T, 576), self.row_align, rows=True)
         return T
 
-    def release(self, keep_len=None):
-        """Returns the pages behind keep_len [B] tokens (all of them without it) of every request, on the current stream."""
+    def release(self, keep_len=None, stream=None):
+        """Returns the pages behind keep_len [B] tokens (all of them without it) of every request."""
         api.block_table_release(self.block_table, self.page_size, self.lengths, self.free_pages, self.n_free, keep_len=keep_len,
-                                dev_status=self.status)
-        if keep_len is None:
-            self.lengths.zero_()
-        else:
-            # (the call leaves a request with a negative length as it was)
-            torch.minimum(self.lengths, torch.where(keep_len < 0, self.lengths, keep_len), out=self.lengths)
+                                dev_status=self.status, stream=stream)
+        with torch.cuda.stream(api._torch_stream(stream, self.lengths.device)):
+            if keep_len is None:
+                self.lengths.zero_()
+            else:
+                # (the call leaves a request with a negative length as it was)
+                torch.minimum(self.lengths, torch.where(keep_len < 0, self.lengths, keep_len), out=self.lengths)

@@ -276,6 +276,26 @@ def test_layer_release_of_lengths_that_are_none(mt):  # noqa: F811
     assert L.n_free.item() == 60 and (L.block_table == -1).all() and (L.lengths == 0).all()
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_layer_release_on_a_stream(mt, raw):  # noqa: F811
+    """Behind a step on the same stream, with work in front of both that takes a while."""
+    L = layer(416)
+    x = tokens(np.random.default_rng(17), 60, 32)
+    new, off, keep = lens([20, 5, 35]), u32([0, 20, 25, 60]), lens([16, 5, 0])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on = s.cuda_stream if raw else s
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    L.step(new, off, **x, stream=on)
+    L.release(keep, stream=on)
+    s.synchronize()
+    assert L.lengths.tolist() == [16, 5, 0] and L.n_free.item() == 58 and L.status.item() == 0
+    L.release(stream=on)
+    s.synchronize()
+    assert L.n_free.item() == 60 and (L.block_table == -1).all() and (L.lengths == 0).all()
+
+
 @pytest.mark.parametrize("row_bytes", [416, 656, 1152])
 def test_layer_keeps_its_scratch_to_itself(mt, row_bytes):  # noqa: F811
     """No buffer that other calls use too: those are replaced by larger ones, and written by whoever comes next."""
