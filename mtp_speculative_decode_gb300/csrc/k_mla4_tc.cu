@@ -38,6 +38,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <stdlib.h>
 
 #include "cache.h"
 #include "common.cuh"
@@ -858,6 +859,8 @@ constexpr double START_PAIRS = 7.0;
 
 bool mla4_tc_supported(const MlaPlan& p) {
   if (p.dtype != MTPSD_FP4_MLA || p.d_latent != 576 || p.d_v != 512 || cc_major() != 10) return false;
+  const char* env = getenv("MTPSD_MLA");
+  if (env && env[0] == 'm') return false;   // "mma": the mma.sync kernel, as for the other formats
   if (p.pool > 0x7ffffffeLL || (int64_t)p.R * p.H > 0x7fffffffLL || p.R > 0x7fffffff / 2 || ceil_div(p.H, m4::HG) * 2 > 65535) return false;
   if (((uintptr_t)p.latent | (uintptr_t)p.q | (uintptr_t)p.out | (uintptr_t)p.ws) % 16) return false;
   return tma_available();

@@ -115,6 +115,94 @@ def test_norm_whose_reciprocal_root_is_infinite(mt, D, rot):  # noqa: F811
     assert ((got - want).abs() <= 2.0 ** -15 * size)[~plain].all()
 
 
+# ----------------------------------------------------------------------------- attention over 4-bit rows
+
+def attention_bound(q, c):
+    """(o, bound of its error, lse, bound) of one row in 64 bits: q [H, 576], c [n, 576].
+
+    A score is the sum of two halves of the dims, 256..511 and the rest.  Each CTA of a pair keeps its own half (float32, at most
+    2^-17 of the sum of the products' magnitudes off) and gets the other rounded to half precision: 2^-11 of it, or 2^-25.  A score off by e
+    weighs its position by 2^e, so the output moves by the weighted distances of the rows from it; probabilities are
+    rounded to bf16 (2^-8), the output too.  A probability below 2^-126 of the reference (which is one of the scores, so the sum is
+    at least 1) is zero: n of them move a value by up to n 2^-126 of the largest entry, all that there is where the other rows hold
+    zeros."""
+    k = SCALE / math.log(2)
+    s = q @ c.T
+    p = np.exp(SCALE * (s - s.max(1, keepdims=True)))
+    lse = SCALE * s.max(1) + np.log(p.sum(1))
+    p /= p.sum(1, keepdims=True)
+    o = p @ c[:, :512]
+    mags = np.abs(q) @ np.abs(c).T * k
+    upper = q[:, 256:512] @ c[:, 256:512].T * k
+    bound, lse_bound = np.zeros_like(o), None
+    for dims, other in ((slice(0, 256), upper), (slice(256, 512), s * k - upper)):
+        eps = math.log(2) * (2.0 ** -11 * np.abs(other) + 2.0 ** -25 + 2.0 ** -17 * mags) + 2.0 ** -20
+        least = (p * np.exp(-eps)).sum(1)
+        for h in range(len(q)):
+            moved = (p[h] * np.expm1(eps[h])) @ np.abs(c[:, dims] - o[h, dims])
+            bound[h, dims] = (moved + (p[h] * np.exp(eps[h])) @ np.abs(c[:, dims]) * 2.0 ** -8) / least[h]
+        if lse_bound is None:              # the first half's CTA writes it
+            lse_bound = np.log((p * np.exp(eps)).sum(1)) + np.abs(lse) * 2.0 ** -22
+    return o, bound + (np.abs(o) + bound) * 2.0 ** -8 + len(c) * 2.0 ** -126 * np.abs(c).max(), lse, lse_bound
+
+
+@pytest.mark.parametrize("H", [128, 48])
+@pytest.mark.parametrize("factor", [1, 10, 40])
+def test_mla_error_of_every_value(mt, factor, H):  # noqa: F811
+    """Scores up to several hundred, rising through the list so that the reference maximum moves in every tile: each value within
+    the bound of the roundings, which stays far below the output (2 % of a row, 15 % of any head)."""
+    rng = np.random.default_rng(78)
+    q, rows, caps, start, pos, idx = mla_case(rng, 1, 2, H, 512, [4000])
+    q = (q.float() * factor).to(torch.bfloat16)
+    c = o4.unpack(rows)
+    idx[0] = np.argsort((q[0].float().numpy() @ c[:4000].T).mean(0))[-512:]
+    lse, st = torch.empty(2, H, device="cuda"), status()
+    out = mt.sparse_mla_decode(q.cuda(), dev(rows), dev(start), u32([0, 2]), dev(pos), dev(idx), SCALE, lse=lse, dev_status=st)
+    assert st.item() == 0
+    for r in range(2):
+        o, bound, want_lse, lse_bound = attention_bound(q[r].double().numpy(), c[idx[r][idx[r] >= 0]])
+        norm = lambda x: np.linalg.norm(x, axis=1)  # noqa: E731
+        assert np.linalg.norm(bound) < 0.02 * np.linalg.norm(o) and (norm(bound) < 0.15 * norm(o)).all()
+        assert (np.abs(out[r].double().cpu().numpy() - o) <= bound).all()
+        assert (np.abs(lse[r].double().cpu().numpy() - want_lse) <= lse_bound).all()
+
+
+@pytest.mark.parametrize("page", [0, 4, 64])
+@pytest.mark.parametrize("H", [16, 128])
+def test_mla_into_a_misaligned_output(mt, H, page, monkeypatch):  # noqa: F811
+    """An output that no TMA store can write takes the kernel for any alignment: short and split lists, codes of 0.5, empty rows."""
+    rng = np.random.default_rng(H + page)
+    for B, W, n_idx, lens in ((1, 1, 1, [0]), (2, 3, 65, [70, 3]), (1, 2, 2048, [5000])):
+        q, rows, caps, start, pos, idx = mla_case(rng, B, W, H, n_idx, lens)
+        rows[0, :256] = 0x11                                     # 0.5 throughout
+        pool, paged, cs = rows, None, dev(start)
+        if page:
+            t = np.full((B, max(otab.n_pages(n, page) for n in caps)), -1, np.int32)
+            ids, at = rng.permutation(sum(otab.n_pages(n, page) for n in caps)), 0
+            pool = rng.integers(0, 256, (len(ids) * page, 416)).astype(np.uint8)
+            for b in range(B):
+                n = otab.n_pages(caps[b], page)
+                t[b, :n] = ids[at:at + n]
+                at += n
+                for s in range(caps[b]):
+                    pool[opaged.slot_of(t, page, b, s)] = rows[start[b] + s]
+            paged, cs = (dev(t), page), None
+        lse, st = torch.empty(B * W, H, device="cuda"), status()
+        buf = torch.full((B * W * H * 512 + 4,), 5.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[2:-2].view(B * W, H, 512)
+        got = mt.sparse_mla_decode(q.cuda(), dev(pool), cs, u32(np.arange(B + 1) * W), dev(pos), dev(idx), SCALE, out=out, lse=lse,
+                                   dev_status=st, paged=paged)
+        assert got is out and st.item() == 0 and (buf[:2] == 5).all() and (buf[-2:] == 5).all()
+        check_mla(out, lse, q, rows, start, W, idx)
+        # the same kernel by choice (the bits of its own sums), and the one for aligned outputs
+        args = (q.cuda(), dev(pool), cs, u32(np.arange(B + 1) * W), dev(pos), dev(idx), SCALE)
+        other = mt.sparse_mla_decode(*args, paged=paged)
+        monkeypatch.setenv("MTPSD_MLA", "mma")
+        assert torch.equal(mt.sparse_mla_decode(*args, paged=paged), out)
+        monkeypatch.delenv("MTPSD_MLA")
+        assert torch.equal(mt.sparse_mla_decode(*args, paged=paged), other) and (n_idx == 1 or not torch.equal(other, out))
+
+
 @pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16", "f32"])
 def test_mla_with_a_misaligned_workspace(mt, kind):  # noqa: F811
     """Split partials at any multiple of 8 bytes: joined by loads that such a buffer allows; at less the call is refused."""
