@@ -17,7 +17,7 @@
 // between the two threads of that head through shared memory.  The reference maximum is lazy: O is rescaled only when a head's
 // maximum grows by more than 2^8.
 // Measured (70 rows, one wave): 1.9 us a pair; 1.5 without the dequantization's arithmetic, 1.07 without the gathers too, 0.77
-// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 213 us (FP8 rows: 357).
+// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 216 us (FP8 rows: 357).
 //
 //   TMEM  [0,128) this CTA's 256 query dims (A operand, bf16 pairs); [128,192) [192,256) scores of even and odd pairs (fp32), P
 //         over their first 32 columns (bf16 pairs); [256,512) O
@@ -75,7 +75,8 @@ constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;      // and room to align
 static_assert(SMEM_BYTES <= 232448 && OFF_C % 1024 == 0 && OFF_BAR % 8 == 0, "shared memory");
 static_assert(4 * 8 * 4096 <= OFF_STG - OFF_C, "the float32 output boxes lie in the drained ring and receive slots");
 constexpr int DEQ_WARP = 8, N_DEQ = 4, GATHER_WARP = DEQ_WARP + N_DEQ, N_GATHER = 2, MMA_WARP = GATHER_WARP + N_GATHER;
-constexpr int THREADS = 32 * (MMA_WARP + 1);
+constexpr int FREE_WARP = MMA_WARP + 1;
+constexpr int THREADS = 32 * (FREE_WARP + 1);
 constexpr int TM_Q = 0, TM_S0 = 128, TM_O = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
@@ -116,9 +117,8 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ void bar_arrive_tx(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
 }
-// Relaxed: what it releases has been read into registers already.
 __device__ __forceinline__ void bar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort_flag, int32_t* status) {
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bar_init(&pv_done[i], 1);
       bar_init(&x_full[2 * i], 1);
       bar_init(&x_full[2 * i + 1], 1);
-      bar_init(&x_free[i], 4);             // one arrival per warp of the other CTA's warpgroup
+      bar_init(&x_free[i], 1);             // the other CTA's FREE_WARP
     }
     for (int i = 0; i < 8; ++i) bar_init(&dec[i], 1);
     for (int i = 0; i < FD / 2; ++i) {     // per pair of tiles
@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t stg_warp = saddr(sm + OFF_STG) + w * XSLOT + quad * 2048;
     const uint32_t x_peer = map_rank(saddr(sm + OFF_X), peer) + w * XSLOT + quad * 2048;
     const uint32_t xfull_peer = map_rank(saddr(x_full), peer) + w * 16;
-    const uint32_t xfree_peer = map_rank(saddr(x_free), peer) + w * 8;
     float* mref = (float*)(sm + OFF_MREF);
     const uint32_t tm_s = tmem + lane_off + TM_S0 + w * 64;
     float m_cur = -INFINITY, l = 0.f;      // this warpgroup's sum, relative to m_cur
@@ -463,8 +462,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) break;
-      __syncwarp();
-      if (lane == 0) bar_arrive_remote(xfree_peer);
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool grow = mt > m_old + RESCALE_LOG2 || (m_old == -INFINITY && mt > -INFINITY);
       const float m_new = grow ? mt : m_old;
@@ -730,6 +727,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           bar_arrive(&c_full[q]);
         }
       }
+      __syncwarp();
+    }
+  } else if (warp == FREE_WARP) {
+    // ------------------------------------------------ receive slots back to the other CTA
+    // Its next copy must not overtake the reads of the four warps here, which have to be released at cluster scope.  A warp that does
+    // nothing else does so: by the softmax warps it held up the chain (226 us for the 192 rows), by the MMA warp too (232), a
+    // relaxed arrival (214) orders nothing.
+    const uint32_t xfree_peer = map_rank(saddr(x_free), peer);
+    for (int P = 0; P < n_pairs; ++P) {
+      // (a warp arrives on dec after its reads)
+      if (!wait_all(&dec[4 * (P & 1) + (lane & 3)], (P >> 1) & 1, abort_flag, p.status)) break;
+      if (lane == 0) bar_arrive_remote(xfree_peer + (P & 1) * 8);
       __syncwarp();
     }
   } else {
