@@ -1,4 +1,5 @@
-// Bounded waits of the head's kernels, and what a kernel whose wait has expired does with its copies (internal header).
+// Bounded waits of the head's kernels and of the attention over 4-bit rows, and what a kernel whose wait has expired does with its
+// copies (internal header).
 //
 // The rule is that of mbar.cuh: the kernel that gives up has flagged MTPSD_STATUS_WAIT_TIMEOUT, stores nothing of the
 // work that it could not finish, waits (bounded again) for its own copies in flight and returns.

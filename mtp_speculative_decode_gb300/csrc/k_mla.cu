@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(256, 1) sparse_mla_bf16_kernel(MlaPlan p, MlaS
 
 // Merge split partials: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  The partials carry
 // `halves` (max, sum) pairs per split: with 2, the two halves of the value dims were accumulated
-// with their own maxima and sums, and each half is merged with its own.
+// with their own maxima and sums, and each half is merged with its own.  A NaN for a maximum stands for a split that was not
+// finished (an expired wait): such values are left as they were.
 template <typename OutT>
 __global__ void mla_combine_kernel(MlaPlan p, int n_splits, int halves, const float* __restrict__ part_o,
                                    const float* __restrict__ part_ml) {
@@ -389,8 +390,13 @@ __global__ void mla_combine_kernel(MlaPlan p, int n_splits, int halves, const fl
   const int64_t rh = blockIdx.x;   // r * H + h
   const float* ml = part_ml + rh * n_splits * halves * 2;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  bool whole[2] = {true, true};
   for (int v = 0; v < halves; ++v) {
-    for (int s = 0; s < n_splits; ++s) m[v] = fmaxf(m[v], ml[(s * halves + v) * 2]);
+    for (int s = 0; s < n_splits; ++s) {
+      const float ms = ml[(s * halves + v) * 2];
+      whole[v] = whole[v] && ms == ms;
+      m[v] = fmaxf(m[v], ms);
+    }
     for (int s = 0; s < n_splits; ++s) {
       const float ms = ml[(s * halves + v) * 2];
       if (ms != -INFINITY) l[v] += exp2f(ms - m[v]) * ml[(s * halves + v) * 2 + 1];
@@ -399,6 +405,7 @@ __global__ void mla_combine_kernel(MlaPlan p, int n_splits, int halves, const fl
   const int dh = p.d_v / halves;
   for (int d = threadIdx.x; d < p.d_v; d += blockDim.x) {
     const int v = halves == 2 && d >= dh ? 1 : 0;
+    if (!whole[v]) continue;
     float acc = 0.f;
     for (int s = 0; s < n_splits; ++s) {
       const float ms = ml[(s * halves + v) * 2];
@@ -409,7 +416,7 @@ __global__ void mla_combine_kernel(MlaPlan p, int n_splits, int halves, const fl
     if constexpr (sizeof(OutT) == 2) *og = __float2bfloat16_rn(acc * inv);
     else *og = acc * inv;
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[rh] = l[0] > 0.f ? (m[0] + log2f(l[0])) / LOG2E : -INFINITY;
+  if (threadIdx.x == 0 && p.lse && whole[0]) p.lse[rh] = l[0] > 0.f ? (m[0] + log2f(l[0])) / LOG2E : -INFINITY;
 }
 
 // The same merge for 512 value dims with 16-byte accesses: four heads per
@@ -428,7 +435,13 @@ __global__ void __launch_bounds__(256) mla_combine512_kernel(MlaPlan p, int n_sp
   const int ms_stride = halves * 2;
   const float* ml = part_ml + rh * n_splits * ms_stride + (halves == 2 ? (t >> 5) * 2 : 0);
   float m = -INFINITY;
-  for (int s = 0; s < n_splits; ++s) m = fmaxf(m, ml[s * ms_stride]);
+  bool whole = true;
+  for (int s = 0; s < n_splits; ++s) {
+    const float ms = ml[s * ms_stride];
+    whole = whole && ms == ms;
+    m = fmaxf(m, ms);
+  }
+  if (!whole) return;
   float l = 0.f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < n_splits; ++s) {

@@ -34,7 +34,7 @@
 // softmax scale and in the output; the rope queries are multiplied by 2^-14 as well, so that both parts of a score have it.
 //
 // Rounding: scores' halves to fp16 (2^-11 of a half), P to bf16 (2^-8), the output to bf16; sums, maxima and O are fp32.
-// Every wait is bounded (2 s) and flags MTPSD_STATUS_WAIT_TIMEOUT on expiry.
+// Every wait is bounded (2 s) and flags MTPSD_STATUS_WAIT_TIMEOUT on expiry; the CTAs then wait for their copies in flight (settle).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,8 +42,8 @@
 
 #include "cache.h"
 #include "common.cuh"
+#include "head_wait.cuh"
 #include "latent4.cuh"
-#include "mbar.cuh"
 
 namespace mtpsd {
 namespace m4 {
@@ -71,7 +71,11 @@ constexpr int B_CFULL = 0, B_CEMPTY = B_CFULL + NPAIR, B_SFULL = B_CEMPTY + NPAI
               B_XFULL = B_PVDONE + 2, B_XFREE = B_XFULL + 4, B_DEC = B_XFREE + 2, B_FFULL = B_DEC + 8, B_FEMPTY = B_FFULL + FD / 2, B_QREADY = B_FEMPTY + FD / 2, B_DRAIN = B_QREADY + 1,
               N_BARS = B_DRAIN + 1;
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;      // and room to align
+// How far each role has come, for a CTA that gives up (settle): tiles whose codes, and whose rope values, a gather warp has fetched;
+// pairs that a dequantizing warp has written; pairs that a softmax warp has sent; pairs that a warpgroup has expected.
+constexpr int OFF_PROG = OFF_MISC + 16;
+constexpr int PG_CODES = 0, PG_ROPE = 2, PG_DEQ = 4, PG_SENT = 8, PG_EXPECTED = 16, N_PROG = 18;
+constexpr int SMEM_BYTES = OFF_PROG + 4 * N_PROG + 1024;      // and room to align
 static_assert(SMEM_BYTES <= 232448 && OFF_C % 1024 == 0 && OFF_BAR % 8 == 0, "shared memory");
 static_assert(4 * 8 * 4096 <= OFF_STG - OFF_C, "the float32 output boxes lie in the drained ring and receive slots");
 constexpr int DEQ_WARP = 8, N_DEQ = 4, GATHER_WARP = DEQ_WARP + N_DEQ, N_GATHER = 2, MMA_WARP = GATHER_WARP + N_GATHER;
@@ -82,7 +86,6 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float UP = 16384.0f;           // 2^14: what the dequantized values lack
 constexpr int MAX_SPLITS = 4;            // splits of a row in one cluster, merged in the kernel
-constexpr unsigned long long WAIT_NS = mbar::DEFAULT_LIMIT_NS;
 
 struct Params {
   int B, R, H, n_idx, n_append;
@@ -122,7 +125,7 @@ __device__ __forceinline__ void bar_arrive_remote(uint32_t cluster_addr) {
 }
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity, volatile int* abort_flag, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar::wait<CLUSTER>(b, parity, abort_flag, status, WAIT_NS));
+  return __all_sync(0xffffffffu, mbar::wait_head<CLUSTER>(b, parity, abort_flag, status));
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
@@ -131,6 +134,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {   // no arrival
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_complete_tx(uint64_t* b, uint32_t bytes) {   // as if so many had come
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, const int* y, uint64_t* bar) {
   asm volatile(
@@ -279,6 +285,47 @@ __device__ __noinline__ void merge_splits(const Params& p, int r, int h0, int lo
   }
 }
 
+// What a CTA that gives up does about its copies in flight: every barrier that has bytes to come gets the arrivals that the roles left
+// out, so that its phase ends with the last of the bytes, and is then waited for (bounded).  peer_prog: the other CTA's OFF_PROG.
+__device__ __noinline__ void settle(uint8_t* sm, uint64_t* bars, uint32_t peer_prog, bool rope, int32_t* status) {
+  const int* prog = (const int*)(sm + OFF_PROG);
+  auto of_pair = [&](int tiles, int P) { return min(max(tiles - 2 * P, 0), 2); };   // tiles of pair P among the first `tiles`
+  // codes and scales; the slots hold the last FD / 2 pairs that were begun
+  const int codes = (max(prog[PG_CODES], prog[PG_CODES + 1]) + 1) / 2;
+  for (int P = max(codes - FD / 2, 0); P < codes; ++P) {
+    uint64_t* b = bars + B_FFULL + P % (FD / 2);
+    for (int g = 0; g < N_GATHER; ++g)
+      if (of_pair(prog[PG_CODES + g], P) < 2) bar_arrive(b);
+    mbar::drain<false>(b, (P / (FD / 2)) & 1, status);
+  }
+  const int ropes = rope ? (max(prog[PG_ROPE], prog[PG_ROPE + 1]) + 1) / 2 : 0;
+  for (int P = max(ropes - NPAIR, 0); P < ropes; ++P) {
+    uint64_t* b = bars + B_CFULL + P % NPAIR;
+    for (int g = 0; g < N_GATHER; ++g)
+      if (of_pair(prog[PG_ROPE + g], P) < 2) bar_arrive(b);
+    for (int d = 0; d < N_DEQ; ++d)
+      if (prog[PG_DEQ + d] <= P) bar_arrive(b);
+    mbar::drain<false>(b, (P / NPAIR) & 1, status);
+  }
+  // scores from the other CTA: of the last pair that any of its warps has sent, 2 KB per warp and half
+  for (int w = 0; w < 2; ++w) {
+    int sent[4], last = 0;
+    uint32_t bytes = 0;
+    for (int q = 0; q < 4; ++q) {
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(sent[q]) : "r"(peer_prog + 4 * (PG_SENT + 4 * w + q)) : "memory");
+      last = max(last, sent[q]);
+    }
+    if (last == 0) continue;
+    for (int q = 0; q < 4; ++q) bytes += sent[q] == last ? XHALF / 4 : 0;
+    for (int half = 0; half < 2; ++half) {
+      uint64_t* b = bars + B_XFULL + 2 * w + half;
+      if (prog[PG_EXPECTED + w] < last) bar_arrive_tx(b, bytes);
+      else if (bytes < XHALF) bar_complete_tx(b, XHALF - bytes);
+      mbar::drain<true>(b, (last - 1) & 1, status);
+    }
+  }
+}
+
 // tm_codes, tm_scale: the rows as bytes, boxes of 128 and 16; tm_rope: their rope values, bf16, 128-byte swizzle; tm_st: the output
 // (bf16) or the split partials (float32).
 template <bool PAGED>
@@ -295,6 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = (volatile int*)(sm + OFF_MISC + 4);
   volatile int* given_up = (volatile int*)(sm + OFF_MISC + 8);   // some CTA of the cluster has aborted
   uint8_t* mask_s = sm + OFF_MASK;
+  volatile int* prog = (volatile int*)(sm + OFF_PROG);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t crank;                          // value half + 2 * split of the cluster
@@ -327,6 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bar_init(drain, 1);
     *abort_flag = 0;
     *given_up = 0;
+    for (int i = 0; i < N_PROG; ++i) prog[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == MMA_WARP) {
@@ -394,7 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tm_s = tmem + lane_off + TM_S0 + w * 64;
     float m_cur = -INFINITY, l = 0.f;      // this warpgroup's sum, relative to m_cur
     bool ok = true;
-    for (int P = w; P < n_pairs && ok; P += 2) {
+    int sent = (n_pairs + 1 - w) / 2, expected = sent;      // pairs of this warpgroup; set where it gives up, the loop carries neither
+    for (int P = w; P < n_pairs; P += 2) {
       const uint32_t par = (P >> 1) & 1;
       if (h == 0) {
         bar_arrive_tx(&x_full[2 * w], XHALF);
@@ -403,7 +453,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the other CTA has taken pair P - 2 out of its slot: slot and staging may be written again
       if (P >= 2) ok = wait_all<true>(&x_free[w], ((P - 2) >> 1) & 1, abort_flag, p.status);
       ok = ok && wait_all(&s_full[w], par, abort_flag, p.status);
-      if (!ok) break;
+      if (!ok) {
+        sent = P / 2;
+        expected = P / 2 + 1;
+        break;
+      }
       fence_after();
       uint32_t sr[64];
       tm_ld32(tm_s, sr);
@@ -433,7 +487,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m_old = -INFINITY;
       if (P > 0) {
         ok = wait_all(&dec[4 * (w ^ 1) + quad], ((P - 1) >> 1) & 1, abort_flag, p.status);
-        if (!ok) break;
+        if (!ok) {
+          sent = expected = P / 2 + 1;
+          break;
+        }
         m_old = mref[h];
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -461,7 +518,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           sr[32 * half + 2 * j + 1] = __float_as_uint(v1);
         }
       }
-      if (!ok) break;
+      if (!ok) {
+        sent = expected = P / 2 + 1;
+        break;
+      }
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool grow = mt > m_old + RESCALE_LOG2 || (m_old == -INFINITY && mt > -INFINITY);
       const float m_new = grow ? mt : m_old;
@@ -472,7 +532,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (__any_sync(0xffffffffu, scale_o)) {
         // after PV(P - 1), and before PV(P): P is published below
         ok = wait_all(&pv_done[(P - 1) & 1], ((P - 1) >> 1) & 1, abort_flag, p.status);
-        if (!ok) break;
+        if (!ok) {
+          sent = expected = P / 2 + 1;
+          break;
+        }
         fence_after();
         const float alpha = scale_o ? ex2(m_old - m_new) : 1.f;
 #pragma unroll 1
@@ -505,6 +568,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&p_full[w]);
+    }
+    if (lane == 0) {
+      prog[PG_SENT + warp] = sent;
+      if (quad == 0) prog[PG_EXPECTED + w] = expected;
     }
     // ------------------------------------------------ output
     float2* ml = (float2*)(sm + OFF_ML);
@@ -614,11 +681,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       dst[m] = (uint32_t)(j >> 1) * CHUNK + (8 * dw + sub) * 128 + (((4 * (j & 1) + ((m + rot) & 3)) ^ sub) << 4);
     const uint32_t src_code = saddr(sm + OFF_F) + (8 * dw + sub) * 128 + 16 * j;
     const uint32_t src_scale = saddr(sm + OFF_F) + F_SCL + 2 * dw * 128 + sub * 16 + 2 * j;
+    int written = n_pairs;
     for (int P = 0; P < n_pairs; ++P) {
       const int q = P % NPAIR, n = P / NPAIR, f0 = (2 * P) % FD;
       uint4 cd[4];
       uint32_t scl[4];
-      if (!wait_all(&f_full[P % (FD / 2)], (P / (FD / 2)) & 1, abort_flag, p.status)) break;
+      if (!wait_all(&f_full[P % (FD / 2)], (P / (FD / 2)) & 1, abort_flag, p.status)) {
+        written = P;
+        break;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {        // tile i / 2, rows + 4 (i % 2)
         const uint32_t at = (uint32_t)(f0 + (i >> 1)) * F_TILE;
@@ -628,7 +699,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src_scale + at + (i & 1) * 128) : "memory");
         scl[i] = v;
       }
-      if (n > 0 && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) break;
+      if (n > 0 && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) {
+        written = P;
+        break;
+      }
       const uint32_t pair = saddr(sm + OFF_C + q * PAIR_STRIDE);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -657,6 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bar_arrive(&f_empty[P % (FD / 2)]);
       }
     }
+    if (lane == 0) prog[PG_DEQ + dw] = written;
   } else if (warp < MMA_WARP) {
     // ------------------------------------------------ gathers: positions 16 gw .. 16 gw + 15 of each tile
     // Two tiles' entries are looked up at once, one per lane (lane = 16 * tile + position): loaded two blocks ahead, their pages one.
@@ -679,6 +754,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int32_t pg1 = PAGED ? page_entry(p, breq, s1) : -1;
     int32_t row = 0;                       // pool rows of the present block (a row outside the map reads zeros)
     uint32_t there = 0;                    // which of them are there
+    int codes = n_tiles, ropes = n_tiles;
     for (int t = 0; t < n_tiles; ++t) {
       if (t % 2 == 0) {                    // the next block becomes the present one
         const int blk = t / 2;
@@ -699,7 +775,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[i] = __shfl_sync(0xffffffffu, row, 16 * (t & 1) + i);
       const int f = t % FD, P = t >> 1, q = P % NPAIR, n = P / NPAIR;
-      if (t >= FD && !(t & 1) && !wait_all(&f_empty[P % (FD / 2)], (t / FD - 1) & 1, abort_flag, p.status)) break;
+      if (t >= FD && !(t & 1) && !wait_all(&f_empty[P % (FD / 2)], (t / FD - 1) & 1, abort_flag, p.status)) {
+        codes = ropes = t;
+        break;
+      }
       const uint32_t dst = saddr(sm + OFF_F + f * F_TILE);
       if (elect_one()) {
         uint64_t* const full = &f_full[P % (FD / 2)];
@@ -713,7 +792,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
       // validity bits and (rank 0) the rope values, straight into their chunk, once the pair buffer is free
-      if (n > 0 && !(t & 1) && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) break;
+      if (n > 0 && !(t & 1) && !wait_all(&c_empty[q], (n - 1) & 1, abort_flag, p.status)) {
+        codes = t + 1;
+        ropes = t;
+        break;
+      }
       if (lane == 0) *(uint16_t*)(mask_s + 8 * q + 4 * (t & 1) + 2 * gw) = (uint16_t)(there >> (16 * (t & 1)));
       __syncwarp();
       if (elect_one()) {
@@ -728,6 +811,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       __syncwarp();
+    }
+    if (lane == 0) {
+      prog[PG_CODES + gw] = codes;
+      prog[PG_ROPE + gw] = ropes;
     }
   } else if (warp == FREE_WARP) {
     // ------------------------------------------------ receive slots back to the other CTA
@@ -790,7 +877,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (elect_one()) commit(drain);
     __syncwarp();
     volatile int dummy = 0;
-    mbar::wait<false>(drain, 0, &dummy, p.status, WAIT_NS);
+    mbar::wait<false>(drain, 0, &dummy, p.status, mbar::DEFAULT_LIMIT_NS);
   }
 
   fence_before();
@@ -804,9 +891,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(saddr((const void*)given_up), c)), "r"(1) : "memory");
   // neither CTA starts another copy into the other's shared memory, and with fused splits every partial of the row is written
   cluster_sync();
-  if (*given_up) {     // copies in flight that nobody waits for (sent by the other CTA, gathered here) land meanwhile; nothing is merged
-    const uint64_t t0 = mbar::globaltimer_ns();
-    while (mbar::globaltimer_ns() - t0 < 200000) {}
+  if (*given_up) {     // nothing is merged, and no CTA leaves while copies to it, or from it, are on their way
+    if (p.n_splits > 1 && !p.fused && threadIdx.x < HG && h0 + (int)threadIdx.x < p.H) {     // (a NaN: not finished)
+      const int64_t rh = (int64_t)r * p.H + h0 + threadIdx.x;
+      p.part_ml[((rh * p.n_splits + split) * 2 + rank) * 2] = __uint_as_float(0x7fffffffu);
+    }
+    if (threadIdx.x == 0) settle(sm, bars, map_rank(saddr((const void*)prog), peer), rank == 0, p.status);
+    __syncwarp();
+    cluster_sync();
     return;
   }
   if (p.fused) {
