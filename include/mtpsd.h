@@ -245,11 +245,15 @@ int mtpsd_topk(const float* scores, int64_t ld, int32_t R, const int64_t* row_le
  * step while the shared indexer selection stays fixed).  Every position must
  * satisfy 0 <= s <= row_pos[r] + row_pos_add; others are skipped and flagged.
  * A row with no valid position gets o = 0 and lse = -inf.
+ * Rounding: products are summed in float32, as are the softmax's maxima and sums and the output; MTPSD_F32 rounds nothing below
+ * that.  The others round each probability to bf16 (2^-8) before it multiplies the values.  In the tensor-core kernels (MTPSD_BF16 and
+ * MTPSD_FP8_DS_MLA with heads a multiple of 128, MTPSD_FP4_MLA) a score is the sum of two CTAs' halves of the dims, and each CTA gets the
+ * other's half rounded to half precision: 2^-11 of that half, which is cut at +-65504 in log2 units (45400 of the natural ones).
  */
 typedef struct {
   int32_t B;
   int32_t R;
-  int32_t n_heads;         /* query heads H: a multiple of 16 for MTPSD_BF16, any for MTPSD_F32 */
+  int32_t n_heads;         /* query heads H: any for MTPSD_F32, else a multiple of 16 */
   int32_t d_latent;        /* 576 */
   int32_t d_v;             /* 512 */
   int32_t n_idx;           /* selected entries per row (row stride of idx) */
@@ -636,7 +640,10 @@ int mtpsd_slot_map(const mtpsd_paged_kv* paged, int32_t B, const uint32_t* token
  * Everything is computed in float32 and rounded once, to the output's type:
  *   MTPSD_BF16, MTPSD_F32   D values per head
  *   MTPSD_FP8_E4M3          128 codes per head (D = 128) and a float32 scale, as mtpsd_quantize_fp8_block128 makes them: what
- *                           mtpsd_indexer_topk reads as q, q_scale, k_cache and k_scale
+ *                           mtpsd_indexer_topk reads as q, q_scale, k_cache and k_scale.  Nothing is rotated between the turn and
+ *                           the codes: an orthogonal rotation of queries and keys changes their product in its roundings only,
+ *                           but both sides have to have it.  Keys filled in this way take queries made in this way; a caller
+ *                           that rotates takes float32 values here and mtpsd_quantize_fp8_block128 behind its rotation
  *   MTPSD_FP8_DS_MLA, MTPSD_FP4_MLA   one latent cache row per token (one head, D = 576, rot_start 512 if anything is turned):
  *                           the rows that mtpsd_pack_latent_fp8 / _fp4 make of the float32 values; keys only
  * A key's output row is slots[t] of a cache of pool_tokens rows (slots NULL: row t); a slot outside it is skipped and flagged

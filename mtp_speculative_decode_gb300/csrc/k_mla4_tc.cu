@@ -17,7 +17,7 @@
 // between the two threads of that head through shared memory.  The reference maximum is lazy: O is rescaled only when a head's
 // maximum grows by more than 2^8.
 // Measured (70 rows, one wave): 1.9 us a pair; 1.5 without the dequantization's arithmetic, 1.07 without the gathers too, 0.77
-// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 216 us (FP8 rows: 357).
+// without exchange and exponentials; the MMAs need 0.65.  192 rows x 128 heads x 2048 positions: 218 us (FP8 rows: 357).
 //
 //   TMEM  [0,128) this CTA's 256 query dims (A operand, bf16 pairs); [128,192) [192,256) scores of even and odd pairs (fp32), P
 //         over their first 32 columns (bf16 pairs); [256,512) O

@@ -4,8 +4,8 @@
 // What it has to move bounds it (each value read and written once); a head's sums never leave its lanes' registers.  A head
 // takes L lanes (4 .. 32), each holding 16-byte vectors of 8 values.  The vectors are dealt out so that the two partners of a
 // half-split rotation lie in the same lane: pair slots hold vector i of the first half and vector i of the second, rest slots what is
-// not turned.  A lane group takes several heads of one token in turn and keeps the token's cosines and sines, and the head's
-// weights, in registers meanwhile; the next head's values are loaded before the present one is computed.
+// not turned.  A lane group takes several heads of one token in turn and keeps the token's cosines and sines in registers
+// meanwhile (the weights come from L1 for each head); the next head's values are loaded before the present one is computed.
 // Shapes that are no multiples of 8 values or of 16 bytes take the element kernel (a warp per head, the head in shared memory).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -337,7 +337,8 @@ __device__ __forceinline__ void run_side(const Args& a, const Side& s, int block
 }
 
 // CTAs of 256 threads per SM that the registers have to allow: the loads in flight carry the bandwidth.  Measured on 16384 x 128
-// heads of 64 rope values (bf16): four CTAs (64 registers) take 126 us, three 133, five 155 (spills).
+// heads of 64 rope values (bf16): four CTAs (64 registers, 40 bytes of spills) take 126 us, three 133, five 155 (256 bytes).  The form
+// of the latent rows and the indexer's heads spills 192 bytes at three CTAs (80 registers).
 constexpr int min_ctas(bool f32, int slots) { return slots >= 8 ? 1 : (slots >= 4 ? (f32 ? 2 : 3) : (f32 ? 3 : 4)); }
 template <bool F32, int QP, int QR, int KP, int KR>
 __global__ void __launch_bounds__(256, min_ctas(F32, 2 * (QP > KP ? QP : KP) + (QR > KR ? QR : KR))) norm_rope_kernel(const __grid_constant__ Args a) {

@@ -636,7 +636,9 @@ class PagedAttention:
 
     B requests of at most max_len tokens (rounded up to whole pages) share n_pages pages; H query heads and H_I indexer heads; at most
     max_tokens tokens a step.  The weights are those of the indexer's key norm (128, with its bias) and of the latent's norm (512); cos_sin [n_pos, 64] turns the
-    first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'.  The scratch of the largest step is held
+    first 64 dims of the indexer's heads and the last 64 of the latent's and the queries'.  Indexer queries and keys are not rotated
+    behind the turn, on either side (see norm_rope's FP8 output in mtpsd.h).  The output is the layer's own buffer, until its next
+    step.  The scratch of the largest step is held
     from the start, about 4 max_tokens max_len bytes for the selection's scores: layers run side by side, and captured steps stay
     valid beside others."""
 
